@@ -285,6 +285,97 @@ ARCHEAD_API int archead_sample_partials(const archead_handle* handle, const uint
 ARCHEAD_API int archead_merge_sample_shards(const float* sample_partials, int32_t n_shards, int32_t T,
                                             int32_t* sampled, archead_stream_t stream);
 
+/* Learning through the frozen head.  archead_logits_lse_argmax gives the
+ * per-token cross-entropies ce[t] = -log p(target[t]); a loss over them gives
+ * g[t] = dLoss / dce[t] (archead_policy_loss, archead_preference_loss, or the
+ * caller's own), and archead_grad_hidden takes g to the hidden states.  (A
+ * library extension; the paper trains nothing through the packed head.)
+ *
+ * archead_grad_hidden: with G[t,v] = exp(y[t,v] - lse[t]) - [v = targets[t]],
+ *   grad_hidden[t,:] = g[t] sum_v G[t,v] W_hat[v,:],
+ * the logits y recomputed, the dense head not formed.
+ *   hidden      [T, d] bf16 bit patterns, as in the forward call.
+ *   targets     [T] int32, lse [T] fp32: as given to and by the forward call.
+ *   grad_ce     [T] fp32, g.  A token with g = 0 gets a row of zeros whatever
+ *               its target, lse and hidden state hold (masked tokens).
+ *   grad_hidden [T, d], 16-byte aligned, bf16 bit patterns or fp32 by
+ *               grad_dtype; every row is written.
+ * A target outside [0, V) with g != 0 gives a row of NaN and sets
+ * ARCHEAD_STATUS_BAD_TARGET.  lse must be the log-sum-exp of the same head and
+ * hidden state: one that is too small by log 2 or more gives NaN.  On a
+ * vocabulary shard lse is the log-sum-exp over all rows (archead_merge_shards)
+ * and targets are global: the result is this shard's share, to be added over
+ * the shards (in fp32).
+ * workspace: >= archead_grad_workspace_bytes(handle, T), 256-byte aligned; the
+ * call needs nothing in it and leaves its own status bits in the status word
+ * (archead_workspace_status).  Calls that may overlap need one each. */
+enum { ARCHEAD_GRAD_BF16 = 0, ARCHEAD_GRAD_F32 = 1 };
+ARCHEAD_API size_t archead_grad_workspace_bytes(const archead_handle* handle, int32_t T);
+ARCHEAD_API int archead_grad_hidden(const archead_handle* handle, const uint16_t* hidden, int32_t T,
+                                    const int32_t* targets, const float* lse, const float* grad_ce,
+                                    void* grad_hidden, int32_t grad_dtype, void* workspace,
+                                    size_t workspace_bytes, archead_stream_t stream);
+
+/* Losses over sequences packed one after another: sequence s holds tokens
+ * cu_seqlens[s] .. cu_seqlens[s+1]-1 (device, int32, nondecreasing, within
+ * [0, T]; a length may be zero).  mask [T] bytes or NULL: a token counts where
+ * it is nonzero; the others, and tokens of no sequence, have no part in any
+ * result, whatever their values (NaN included), and get a gradient of 0.
+ * T <= 2^20; T = 0 gives zeros.  Every pointer is device memory, 4-byte
+ * aligned (mask: any); arrays on 16 bytes are read faster.  workspace: >=
+ * archead_loss_workspace_bytes(number of sequences), 256-byte aligned, nothing
+ * needed in it; calls that may overlap need one each.  Results do not depend
+ * on timing.  EINVAL for options outside the ranges given.
+ *
+ * archead_policy_loss: clipped policy loss with a KL term.  Per counted token,
+ *   D = ce_old - ce (the log-ratio to the sampling policy), r = exp(D),
+ *   l = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high))
+ *       + kl_coef (exp(d) - 1 - d),  d = ce - ce_ref  (none if ce_ref is NULL),
+ * loss = scale * sum of w l, grad_ce = dloss / dce, with w = 1 / counted tokens
+ * (REDUCE_TOKENS), 1 / (n * counted tokens of the sequence), n the sequences
+ * with any (REDUCE_SEQUENCES), or 1 (REDUCE_SUM).  At a border of the clipping
+ * the ratio counts as inside.
+ *   advantages  [T] (PER_TOKEN) or [n_sequences] (PER_SEQUENCE).
+ *   cu_seqlens  NULL: one sequence of T tokens (n_sequences = 1).
+ *   stats [3]   means over the counted tokens: share of clipped tokens (their
+ *               ratio has no gradient), exp(D) - 1 - D, exp(d) - 1 - d.
+ * 0 <= clip_low <= 1, clip_high >= 0, kl_coef and scale finite. */
+enum { ARCHEAD_REDUCE_TOKENS = 0, ARCHEAD_REDUCE_SEQUENCES = 1, ARCHEAD_REDUCE_SUM = 2 };
+enum { ARCHEAD_PER_TOKEN = 0, ARCHEAD_PER_SEQUENCE = 1 };
+typedef struct archead_policy_options {
+  double clip_low, clip_high, kl_coef, scale;
+  int32_t reduction, advantage_per;
+} archead_policy_options;
+ARCHEAD_API size_t archead_loss_workspace_bytes(int32_t n_sequences);
+ARCHEAD_API int archead_policy_loss(const float* ce, const float* ce_old, const float* advantages,
+                                    const float* ce_ref, const uint8_t* mask, const int32_t* cu_seqlens,
+                                    int32_t T, int32_t n_sequences, const archead_policy_options* options,
+                                    float* loss, float* grad_ce, float* stats, void* workspace,
+                                    size_t workspace_bytes, archead_stream_t stream);
+
+/* archead_preference_loss: paired log-ratios.  Sequences 0 .. n_pairs-1 are the
+ * chosen ones, n_pairs .. 2 n_pairs - 1 the rejected ones of the same pairs.
+ * With s the sum of ce_ref - ce over a sequence's counted tokens (of -ce if
+ * ce_ref is NULL; their mean if average; 0 if none), D = s_chosen - s_rejected
+ * and h = beta D - margin, a pair's loss is
+ *   SIGMOID  (1 - e) log(1 + exp(-h)) + e log(1 + exp(h)), e = label_smoothing
+ *   HINGE    max(0, 1 - h)
+ *   SQUARED  (D - 1 / (2 beta))^2
+ * loss = scale * their mean, grad_ce = dloss / dce, rewards [2][n_pairs] =
+ * beta s of the chosen and of the rejected sequences.
+ * beta > 0; margin finite, 0 for SQUARED; label_smoothing in [0, 1/2], 0 unless
+ * SIGMOID; scale finite. */
+enum { ARCHEAD_PREFERENCE_SIGMOID = 0, ARCHEAD_PREFERENCE_HINGE = 1, ARCHEAD_PREFERENCE_SQUARED = 2 };
+typedef struct archead_preference_options {
+  double beta, margin, label_smoothing, scale;
+  int32_t kind, average;
+} archead_preference_options;
+ARCHEAD_API int archead_preference_loss(const float* ce, const float* ce_ref, const uint8_t* mask,
+                                        const int32_t* cu_seqlens, int32_t T, int32_t n_pairs,
+                                        const archead_preference_options* options, float* loss, float* grad_ce,
+                                        float* rewards, void* workspace, size_t workspace_bytes,
+                                        archead_stream_t stream);
+
 /* Read (and with clear != 0, reset) the device status word of a workspace:
  * a bitwise OR of ARCHEAD_STATUS_* since the last clear.  Synchronises the
  * stream.  Returns ARCHEAD_ETIMEOUT if ARCHEAD_STATUS_WAIT_TIMEOUT is set. */

@@ -8,3 +8,4 @@ from .archead_oracle import (bf16_decode, build_packed_head, component_bytes, co
                              damped_metric, dequantize, dequantized_factors, fp16_decode, fp16_encode,
                              logits, logits_factored, lse_argmax_ce, metric_objective, packed_bytes,
                              quantize_symmetric, tolerance, truncated_svd, w_hat_rows, QRANGE)
+from .archead_learning import ce_gradient, dense_rows, hidden_f64, policy_loss, preference_loss  # noqa: F401

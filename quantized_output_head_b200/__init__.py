@@ -37,6 +37,8 @@ EXPORTED = (
     "archead_logits_host",
     "archead_forward_kernel", "archead_set_vocab_shard", "archead_shard_partials", "archead_merge_shards",
     "archead_sample", "archead_sample_partials", "archead_merge_sample_shards",
+    "archead_grad_workspace_bytes", "archead_grad_hidden", "archead_loss_workspace_bytes", "archead_policy_loss",
+    "archead_preference_loss",
 )
 
 
@@ -47,6 +49,21 @@ class ArcheadDesc(ctypes.Structure):
 class ArcheadHostComponents(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("L", "s_L", "R", "s_R", "q", "s_res", "A", "s_A", "B", "s_B")]
 
+
+class ArcheadPolicyOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("clip_low", "clip_high", "kl_coef", "scale")] + [
+        (n, ctypes.c_int32) for n in ("reduction", "advantage_per")]
+
+
+class ArcheadPreferenceOptions(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("beta", "margin", "label_smoothing", "scale")] + [
+        (n, ctypes.c_int32) for n in ("kind", "average")]
+
+
+GRAD_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+REDUCTIONS = {"tokens": 0, "sequences": 1, "sum": 2}
+ADVANTAGES = {"token": 0, "sequence": 1}
+PREFERENCES = {"sigmoid": 0, "hinge": 1, "squared": 2}
 
 _vp, _sz, _i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32
 _sig = {
@@ -77,6 +94,13 @@ _sig = {
     "archead_sample_partials": (ctypes.c_int, [_vp, _vp, _i32, ctypes.c_float, ctypes.c_uint64, ctypes.c_uint64, _vp,
                                                _vp, _sz, _vp]),
     "archead_merge_sample_shards": (ctypes.c_int, [_vp, _i32, _i32, _vp, _vp]),
+    "archead_grad_workspace_bytes": (_sz, [_vp, _i32]),
+    "archead_grad_hidden": (ctypes.c_int, [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "archead_loss_workspace_bytes": (_sz, [_i32]),
+    "archead_policy_loss": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, ctypes.POINTER(ArcheadPolicyOptions),
+                                           _vp, _vp, _vp, _vp, _sz, _vp]),
+    "archead_preference_loss": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, ctypes.POINTER(ArcheadPreferenceOptions),
+                                               _vp, _vp, _vp, _vp, _sz, _vp]),
     "archead_test_decode_waits": (ctypes.c_int, [_vp, ctypes.c_uint64, ctypes.c_int]),
     "archead_free": (None, [_vp]),
     "archead_last_cuda_error": (ctypes.c_int, []),
@@ -310,6 +334,40 @@ class PackedHead:
                                    _stream_ptr(None)), "archead_sample")
         return out, lse, am
 
+    # ------------------------------------------------------------ gradient
+    def grad_workspace_bytes(self, T: int) -> int:
+        return int(_lib.archead_grad_workspace_bytes(self.handle, int(T)))
+
+    def grad_hidden(self, hidden: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, grad_ce: torch.Tensor,
+                    out_dtype: torch.dtype = torch.bfloat16, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Gradient [T, d] of a loss with respect to the hidden states, from its
+        gradient grad_ce [T] (fp32) with respect to the cross-entropies that
+        lse_argmax(hidden, targets) gave with lse [T] (fp32).  The head is
+        frozen.  A token with grad_ce 0 gets zeros whatever its target and lse
+        hold.  out_dtype: bfloat16, or float32 (to add up vocabulary shards,
+        whose lse is the merged one).  workspace: a uint8 tensor of
+        grad_workspace_bytes(T) on this device, for callers that want its status
+        word (status()); by default one is allocated for the call."""
+        _check_hidden(hidden, self.d)
+        T = int(hidden.shape[0])
+        if out_dtype not in GRAD_DTYPES:
+            raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+        if hidden.device != self.device:
+            raise ValueError("hidden must be on the head's device")
+        targets = targets.to(device=self.device, dtype=torch.int32).contiguous()
+        if targets.shape != (T,):
+            raise ValueError("targets must hold one id per token")
+        lse, grad_ce = _check_tokens("lse", lse, T, self.device), _check_tokens("grad_ce", grad_ce, T, self.device)
+        with torch.cuda.device(self.device):
+            out = torch.empty((T, self.d), dtype=out_dtype, device=self.device)
+            if workspace is None:
+                workspace = torch.empty(self.grad_workspace_bytes(T), dtype=torch.uint8, device=self.device)
+            _check(_lib.archead_grad_hidden(self.handle, hidden.data_ptr(), T, targets.data_ptr(), lse.data_ptr(),
+                                            grad_ce.data_ptr(), out.data_ptr(), GRAD_DTYPES[out_dtype],
+                                            workspace.data_ptr(), workspace.numel(), _stream_ptr(None)),
+                   "archead_grad_hidden")
+        return out
+
     # --------------------------------------------------- vocabulary shards
     def set_vocab_shard(self, row_offset: int, vocab_total: int) -> None:
         """This head holds global rows [row_offset, row_offset + V) of a
@@ -442,6 +500,109 @@ def merge_sample_shards(parts: torch.Tensor) -> torch.Tensor:
         _check(_lib.archead_merge_sample_shards(parts.data_ptr(), n, T, out.data_ptr(), _stream_ptr(None)),
                "archead_merge_sample_shards")
     return out
+
+
+# ------------------------------------------------- losses over cross-entropies
+def policy_loss(ce: torch.Tensor, ce_old: torch.Tensor, advantages: torch.Tensor,
+                cu_seqlens: Optional[torch.Tensor] = None, *, mask: Optional[torch.Tensor] = None,
+                ce_ref: Optional[torch.Tensor] = None, clip_low: float = 0.2, clip_high: float = 0.2,
+                kl_coef: float = 0.0, reduction: str = "tokens", advantage_per: str = "token", scale: float = 1.0):
+    """Clipped policy loss over the cross-entropies ce [T] of sampled tokens
+    (lse_argmax), with an optional KL term to a reference; returns (loss [],
+    dloss/dce [T], stats [3]), fp32, all on ce's device.
+
+    ce_old, ce_ref: the same tokens' cross-entropies under the policy that
+    sampled them and under the reference.  cu_seqlens [S + 1]: sequence s holds
+    tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (default: one sequence).  mask
+    [T] bool: the tokens that count.  advantages: [T], or [S] with
+    advantage_per="sequence".  reduction: "tokens" (mean over counted tokens),
+    "sequences" (mean over sequences of their means) or "sum".  stats: share of
+    clipped tokens, mean divergence from ce_old's policy, from the reference."""
+    T = _token_count("ce", ce)
+    device = ce.device
+    if reduction not in REDUCTIONS or advantage_per not in ADVANTAGES:
+        raise ValueError(f"reduction must be one of {tuple(REDUCTIONS)}, advantage_per of {tuple(ADVANTAGES)}")
+    S = 1
+    if cu_seqlens is not None:
+        cu_seqlens, S = _check_cu(cu_seqlens, device)
+    ce, ce_old = _check_tokens("ce", ce, T, device), _check_tokens("ce_old", ce_old, T, device)
+    advantages = _check_tokens("advantages", advantages, T if advantage_per == "token" else S, device)
+    if ce_ref is not None:
+        ce_ref = _check_tokens("ce_ref", ce_ref, T, device)
+    if mask is not None:
+        mask = _check_mask(mask, T, device)
+    opts = ArcheadPolicyOptions(clip_low, clip_high, kl_coef, scale, REDUCTIONS[reduction], ADVANTAGES[advantage_per])
+    with torch.cuda.device(device):
+        grad, few, ws = _loss_buffers(T, 4, S, device)
+        at = few.data_ptr()
+        _check(_lib.archead_policy_loss(ce.data_ptr(), ce_old.data_ptr(), advantages.data_ptr(), _ptr(ce_ref), _ptr(mask),
+                                        _ptr(cu_seqlens), T, S, ctypes.byref(opts), at, grad.data_ptr(), at + 4,
+                                        ws.data_ptr(), ws.numel(), _stream_ptr(None)), "archead_policy_loss")
+    return few[0], grad, few[1:]
+
+
+def preference_loss(ce: torch.Tensor, cu_seqlens: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
+                    ce_ref: Optional[torch.Tensor] = None, beta: float = 0.1, kind: str = "sigmoid",
+                    label_smoothing: float = 0.0, margin: float = 0.0, average: bool = False, scale: float = 1.0):
+    """Preference loss over paired log-ratios; returns (loss [], dloss/dce [T],
+    rewards [2, N]), fp32, all on ce's device.
+
+    cu_seqlens [2N + 1]: sequences 0 .. N-1 are the chosen ones, N .. 2N-1 the
+    rejected ones of the same pairs, packed one after another in ce [T] (and in
+    ce_ref, the reference model's cross-entropies; None for a reference-free
+    loss).  mask [T] bool: the tokens that count.  kind: "sigmoid" (with
+    label_smoothing and margin), "hinge" (with margin) or "squared"; average:
+    a sequence's mean log-ratio instead of its sum."""
+    T = _token_count("ce", ce)
+    device = ce.device
+    if kind not in PREFERENCES:
+        raise ValueError(f"kind must be one of {tuple(PREFERENCES)}")
+    cu_seqlens, S = _check_cu(cu_seqlens, device)
+    if S % 2:
+        raise ValueError("cu_seqlens must hold 2N + 1 offsets: N chosen, then N rejected sequences")
+    ce = _check_tokens("ce", ce, T, device)
+    if ce_ref is not None:
+        ce_ref = _check_tokens("ce_ref", ce_ref, T, device)
+    if mask is not None:
+        mask = _check_mask(mask, T, device)
+    opts = ArcheadPreferenceOptions(beta, margin, label_smoothing, scale, PREFERENCES[kind], 1 if average else 0)
+    with torch.cuda.device(device):
+        grad, few, ws = _loss_buffers(T, 1 + S, S, device)
+        at = few.data_ptr()
+        _check(_lib.archead_preference_loss(ce.data_ptr(), _ptr(ce_ref), _ptr(mask), cu_seqlens.data_ptr(), T, S // 2,
+                                            ctypes.byref(opts), at, grad.data_ptr(), at + 4, ws.data_ptr(), ws.numel(),
+                                            _stream_ptr(None)), "archead_preference_loss")
+    return few[0], grad, few[1:].view(2, S // 2)
+
+
+def _loss_buffers(T, n_few, S, device):
+    """The gradient, the small outputs (one tensor) and the workspace of a loss call."""
+    return (torch.empty(T, dtype=torch.float32, device=device), torch.empty(n_few, dtype=torch.float32, device=device),
+            torch.empty(_lib.archead_loss_workspace_bytes(S), dtype=torch.uint8, device=device))
+
+
+def _token_count(name, x) -> int:
+    if x.dim() != 1 or not x.is_cuda:
+        raise ValueError(f"{name} must be a one-dimensional CUDA tensor")
+    return x.shape[0]
+
+
+def _check_tokens(name, x, n, device) -> torch.Tensor:
+    if x.dtype != torch.float32 or x.shape != (n,) or x.device != device:
+        raise ValueError(f"{name} must be a float32 tensor of {n} elements on {device}")
+    return x.contiguous()
+
+
+def _check_mask(mask, T, device) -> torch.Tensor:
+    if mask.dtype not in (torch.bool, torch.uint8) or mask.shape != (T,) or mask.device != device:
+        raise ValueError(f"mask must be a bool or uint8 tensor of {T} elements on {device}")
+    return mask.contiguous()
+
+
+def _check_cu(cu_seqlens, device):
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype not in (torch.int32, torch.int64):
+        raise ValueError("cu_seqlens must be a one-dimensional int32 tensor of one offset more than sequences")
+    return cu_seqlens.to(device=device, dtype=torch.int32).contiguous(), cu_seqlens.shape[0] - 1
 
 
 def _check_hidden(hidden: torch.Tensor, d: int) -> None:

@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libarchead.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
-SOURCES = ["pack.cu", "api.cu", "decode.cu", "prologue.cu", "static_ws.cu", "actprep.cu", "tcgemm.cu"]
+SOURCES = ["pack.cu", "api.cu", "decode.cu", "prologue.cu", "static_ws.cu", "actprep.cu", "tcgemm.cu",
+           "grad.cu", "loss.cu"]
 BUILDER_SOURCES = ["builder.cu"]
 BUILDER_LIB = os.path.join(PKG, "libarchead_build.so")
 FORWARD_HEADERS = ["archead.h"]

@@ -47,28 +47,13 @@ int forward_tc(const archead_handle* h, const uint16_t* hidden, int32_t T, const
   float4* partials = reinterpret_cast<float4*>(wb + w.tpartials);
   float* tgt = reinterpret_cast<float*>(wb + w.tgt);
 
-  ActParams ap{};
+  ActParams ap = act_params(*h);
   ap.hidden = hidden;
-  ap.R = reinterpret_cast<const int8_t*>(h->arena + L.off_R);
-  ap.s_R = reinterpret_cast<const uint16_t*>(h->arena + L.off_sR);
-  ap.B = reinterpret_cast<const int8_t*>(h->arena + L.off_B);
-  ap.s_B = reinterpret_cast<const uint16_t*>(h->arena + L.off_sB);
   ap.targets = targets;
   ap.status = status;
   ap.xop = xop;
   ap.cinv = cinv;
   ap.T = T;
-  ap.d = L.d;
-  ap.rcp = L.rcp;
-  ap.Kz = L.Kz;
-  ap.Kc = Kc;
-  ap.g_B = L.g_B;
-  ap.V = L.V;
-  ap.v_total = h->v_total;
-  ap.alpha = h->tc_alpha;
-  ap.beta = h->tc_beta;
-  ap.gamma = h->tc_gamma;
-  ap.mseg = h->tc_mseg;
   // The K-split partials borrow the region of the tensor-core partials: the
   // tensor-core kernel writes there only after this grid has completed.
   const size_t part_bytes = static_cast<size_t>(T) * tc_n_mt128(L) * 16;

@@ -26,6 +26,7 @@ struct archead_handle {
   // the shape can take it.
   bool tc_ok;
   int tc_alpha, tc_beta, tc_gamma, tc_mseg;
+  int tc_rho_c, tc_rho_r;   // the same for the dequantised rows of R and B (gradient)
   int row0;                 // vocabulary shard: global id of row 0, and the global vocabulary size
   int v_total;
   cudaEvent_t ev_before;    // optional profiling events (not owned)
@@ -98,6 +99,29 @@ inline WsLayout ws_layout(const archead_handle& h, int T) {
   return w;
 }
 
+// Arguments of the activation kernel that the head alone sets; the caller adds
+// hidden, targets, status, xop, cinv, T and the K-split scratch.
+inline ActParams act_params(const archead_handle& h) {
+  const Layout& L = h.L;
+  ActParams ap{};
+  ap.R = reinterpret_cast<const int8_t*>(h.arena + L.off_R);
+  ap.s_R = reinterpret_cast<const uint16_t*>(h.arena + L.off_sR);
+  ap.B = reinterpret_cast<const int8_t*>(h.arena + L.off_B);
+  ap.s_B = reinterpret_cast<const uint16_t*>(h.arena + L.off_sB);
+  ap.d = L.d;
+  ap.rcp = L.rcp;
+  ap.Kz = L.Kz;
+  ap.Kc = tc_kc(L);
+  ap.g_B = L.g_B;
+  ap.V = L.V;
+  ap.v_total = h.v_total;
+  ap.alpha = h.tc_alpha;
+  ap.beta = h.tc_beta;
+  ap.gamma = h.tc_gamma;
+  ap.mseg = h.tc_mseg;
+  return ap;
+}
+
 // Kernel launchers and attributes (decode.cu, prologue.cu).
 void decode_smem_plan(DecodeParams& p, int g_steps);
 size_t decode_smem_bytes(const DecodeParams& p);
@@ -114,6 +138,8 @@ void tc_smem_plan(TcParams& p);
 size_t tc_smem_bytes(const TcParams& p);
 size_t tc_smem_max();
 cudaError_t tc_set_attributes();
+cudaError_t tc_encode_map(CUtensorMap* map, const uint16_t* base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                          int box_rows);
 cudaError_t tc_encode_xmap(CUtensorMap* map, const uint16_t* xop, int T, int Kc, int BN);
 cudaError_t launch_tc(const TcParams& p, const CUtensorMap& map, int grid, cudaStream_t stream);
 cudaError_t launch_tc_merge(const float4* partials, int n_mt128, int T, const int32_t* targets, const float* tgt,
@@ -121,6 +147,9 @@ cudaError_t launch_tc_merge(const float4* partials, int n_mt128, int T, const in
                             cudaStream_t stream);
 cudaError_t launch_shard_merge(const float4* parts, int n, int T, float* lse, int32_t* argmax, float* ce,
                                cudaStream_t stream);
+
+// Gradient of the head (grad.cu).
+cudaError_t grad_set_attributes();
 
 // Thread-local record of the last CUDA error (api.cu).
 int set_cuda_error(cudaError_t e);

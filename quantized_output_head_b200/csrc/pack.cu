@@ -207,6 +207,9 @@ void plan_tc(archead_handle* h, const archead_host_components& C, int smem_optin
   if (L.r_c > 0) m = std::min(m, h->tc_beta - h->e_B);
   if (L.r_r > 0) m = std::min(m, h->tc_gamma - h->e_B);
   h->tc_mseg = m;
+  h->tc_rho_c = L.r_c > 0 ? kScaleExp - exp_above(128.0 * max_abs_half(C.s_R, L.r_c)) : 0;
+  h->tc_rho_r =
+      L.r_r > 0 ? kScaleExp - exp_above(128.0 * max_abs_half(C.s_B, static_cast<size_t>(L.r_r) * (L.d / L.g_B))) : 0;
   // The activation kernel folds the group scales of B at 64-column block ends.
   h->tc_ok = (L.g_B % kTcBK == 0) && tc_smem_max() <= static_cast<size_t>(smem_optin);
 }
@@ -325,6 +328,7 @@ extern "C" ARCHEAD_API int archead_pack_load(const archead_desc* desc, const arc
   plan_tc(h, *comps, optin);
   e = decode_set_attributes(L.g_steps, static_cast<size_t>(optin));
   if (e == cudaSuccess && h->tc_ok) e = tc_set_attributes();
+  if (e == cudaSuccess) e = grad_set_attributes();
   if (e != cudaSuccess) {
     delete h;
     return set_cuda_error(e);

@@ -769,8 +769,11 @@ EncodeTiled g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-// Tensor map of X [T, Kc] fp16: boxes of 64 columns x BN rows, 128-byte swizzle.
-cudaError_t tc_encode_xmap(CUtensorMap* map, const uint16_t* xop, int T, int Kc, int BN) {
+// Tensor map of a row-major fp16 matrix [rows, cols] with `pitch` elements per
+// row (a multiple of 8): boxes of 64 columns x box_rows rows, 128-byte swizzle,
+// zeros outside the matrix.
+cudaError_t tc_encode_map(CUtensorMap* map, const uint16_t* base, uint64_t cols, uint64_t rows, uint64_t pitch,
+                          int box_rows) {
   std::call_once(g_encode_once, []() {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q{};
@@ -779,14 +782,19 @@ cudaError_t tc_encode_xmap(CUtensorMap* map, const uint16_t* xop, int T, int Kc,
       g_encode = reinterpret_cast<EncodeTiled>(fn);
   });
   if (g_encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(Kc), static_cast<cuuint64_t>(T)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(Kc) * 2};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kTcBK), static_cast<cuuint32_t>(BN)};
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(kTcBK), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t*>(xop), dims, strides,
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<uint16_t*>(base), dims, strides,
                               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// X [T, Kc]: boxes of 64 columns x BN rows.
+cudaError_t tc_encode_xmap(CUtensorMap* map, const uint16_t* xop, int T, int Kc, int BN) {
+  return tc_encode_map(map, xop, Kc, T, Kc, BN);
 }
 
 cudaError_t launch_tc(const TcParams& p, const CUtensorMap& map, int grid, cudaStream_t stream) {

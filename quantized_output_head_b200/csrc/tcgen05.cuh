@@ -60,6 +60,17 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
       : "memory");
 }
 
+// The same with A in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Instruction descriptor of kind::f16: fp16 A and B, both K-major, fp32 D,
 // M x N tile (M = 128 here, N a multiple of 16 up to 256).
 __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N) {
@@ -68,6 +79,9 @@ __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N) {
          | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
+
+// Bit of the instruction descriptor that makes B MN-major (stored [K][N]).
+constexpr uint32_t kTcIdescBmn = 1u << 16;
 
 // Shared-memory matrix descriptor of a K-major operand tile stored with the
 // 128-byte swizzle: rows of 128 bytes (64 fp16), 8-row atoms of 1024 bytes.
@@ -80,6 +94,20 @@ __device__ __forceinline__ uint64_t smem_desc_k128(uint32_t saddr) {
   d |= static_cast<uint64_t>(1024u >> 4) << 32;                 // stride byte offset: 8 rows
   d |= static_cast<uint64_t>(1u) << 46;                         // descriptor version
   d |= static_cast<uint64_t>(2u) << 61;                         // 128-byte swizzle
+  return d;
+}
+
+// The descriptor of an MN-major operand tile (stored [K][N]) with the 128-byte
+// swizzle: blocks of 64 N values, each K rows of 128 bytes, block_bytes apart
+// (the leading byte offset); 8-row groups along K are 1024 bytes apart.
+// Advancing along K adds 128 bytes per row (2048 per K = 16 step).
+__device__ __forceinline__ uint64_t smem_desc_mn128(uint32_t saddr, uint32_t block_bytes) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(block_bytes >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
   return d;
 }
 
@@ -187,5 +215,7 @@ __device__ __forceinline__ void unpack_int8_signed(uint32_t w0, uint32_t w1, uin
 // registers (a0, a2) of row gr into TMEM columns (2cc, 2cc + 1), so TMEM
 // element e of the block holds column 2*(e/4) + (e & 1) + 8*((e/2) & 1).
 __host__ __device__ constexpr int tc_kpos(int k) { return 4 * ((k & 7) >> 1) + 2 * (k >> 3) + (k & 1); }
+// Its inverse: the logical column at position e.
+__host__ __device__ constexpr int tc_kcol(int e) { return 2 * (e >> 2) + (e & 1) + 8 * ((e >> 1) & 1); }
 
 }  // namespace archead
