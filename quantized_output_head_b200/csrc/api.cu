@@ -256,6 +256,13 @@ int forward(const archead_handle* h, const uint16_t* hidden, int32_t T, const in
 
 }  // namespace
 
+int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float* logits, void* ws, size_t ws_bytes,
+                   cudaStream_t stream) {
+  archead_handle q = h;
+  q.ev_before = q.ev_after = nullptr;
+  return forward(&q, hidden, T, nullptr, logits, nullptr, nullptr, nullptr, ws, ws_bytes, stream);
+}
+
 int set_cuda_error(cudaError_t e) {
   g_last_cuda_error = static_cast<int>(e);
   return ARCHEAD_ECUDA;

@@ -228,7 +228,7 @@ __device__ __forceinline__ float4 packed_row4(const DequantParams& p, const uint
   return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
 }
 
-// One block per token: S from the tiles' partial sums (in a fixed order), then
+// Blocks of 1024 columns per token: S from the tiles' partial sums (in a fixed order), then
 // dX (added over the K splits) / S + (1/S - 1) W~[target]; the residual columns
 // stay fp32 in the first split's place, the low-rank ones become the fp16
 // operand dz [T][Kz'].
@@ -240,13 +240,15 @@ struct DxParams {
   float* dx;
   size_t split_stride;
   uint16_t* dz;
-  int32_t n_ssum, tokens, splits, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
+  int32_t n_ssum, tokens, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
+  int32_t splits, splits_last, last;               // partial dX of columns below `last`, and of the rest
 };
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   __shared__ float part[8];
   const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q0 = blockIdx.y * blockDim.x + threadIdx.x, dq = gridDim.y * blockDim.x;
   if (p.grad[t] == 0.f) {     // its row of dX is zero, S has no meaning
-    for (int q = threadIdx.x; q < (p.Kc - p.d) / 4; q += blockDim.x)
+    for (int q = q0; q < (p.Kc - p.d) / 4; q += dq)
       *reinterpret_cast<uint2*>(p.dz + static_cast<size_t>(t) * (p.Kc - p.d) + 4 * q) = make_uint2(0u, 0u);
     return;
   }
@@ -268,9 +270,10 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   const float c = (r - 1.f) * static_cast<float>(1 << kGradScale);
   const uint8_t* blk = p.rows.mtiles + static_cast<size_t>(has ? target / kMT : 0) * p.rows.mblk_bytes;
   float* dx = p.dx + static_cast<size_t>(t) * p.Kc;
-  for (int q = threadIdx.x; q < p.Kc / 4; q += blockDim.x) {
+  for (int q = q0; q < p.Kc / 4; q += dq) {
     float4 v = reinterpret_cast<const float4*>(dx)[q];
-    for (int s = 1; s < p.splits; ++s) {
+    const int n = 4 * q < p.last ? p.splits : p.splits_last;
+    for (int s = 1; s < n; ++s) {
       const float4 x = reinterpret_cast<const float4*>(dx + s * p.split_stride)[q];
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
@@ -330,18 +333,21 @@ struct GemmSmem {
   int* abort_flag;
 };
 
-__device__ __forceinline__ bool g_aborted(const GemmSmem& s) { return *reinterpret_cast<volatile int*>(s.abort_flag) != 0; }
+__device__ __forceinline__ bool aborted(int* flag) { return *reinterpret_cast<volatile int*>(flag) != 0; }
 
 // Bounded, warp-uniform wait; on expiry raises the status and the abort flag.
-__device__ __forceinline__ bool g_wait(const GemmSmem& s, uint32_t bar, uint32_t parity, uint32_t* status) {
+__device__ __forceinline__ bool warp_wait(int* abort_flag, uint32_t bar, uint32_t parity, uint32_t* status) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  bool ok = !g_aborted(s) && mbar_wait(bar, parity);
+  bool ok = !aborted(abort_flag) && mbar_wait(bar, parity);
   ok = __all_sync(0xffffffffu, ok);
-  if (!ok && (threadIdx.x & 31) == 0 && !g_aborted(s)) {
-    *reinterpret_cast<volatile int*>(s.abort_flag) = 1;
+  if (!ok && (threadIdx.x & 31) == 0 && !aborted(abort_flag)) {
+    *reinterpret_cast<volatile int*>(abort_flag) = 1;
     atomicOr(status, static_cast<uint32_t>(ARCHEAD_STATUS_WAIT_TIMEOUT));
   }
   return ok;
+}
+__device__ __forceinline__ bool g_wait(const GemmSmem& s, uint32_t bar, uint32_t parity, uint32_t* status) {
+  return warp_wait(s.abort_flag, bar, parity, status);
 }
 
 struct GemmUnit {
@@ -611,40 +617,421 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------- few tokens: G, G W~
+// G from the forward kernels' logits (fp32 [T][V]): one block per (token, piece
+// of kGPiece rows), with the piece's sum of exp(y - lse).
+constexpr int kGPiece = 2048;
+struct GParams {
+  const float* y;
+  const float* lse;
+  const float* grad;
+  const int32_t* targets;
+  uint16_t* G;                // [T][pitch]
+  float* ssum;                // [pieces][T]
+  int32_t T, V, Vp, row0, pitch;
+};
+__global__ void __launch_bounds__(256) g_kernel(const GParams p) {
+  __shared__ float part[8];
+  const int t = blockIdx.y, v0 = blockIdx.x * kGPiece, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool live = p.grad[t] != 0.f;   // (its lse and target may be anything otherwise)
+  const float lse = live ? p.lse[t] : 0.f;
+  const int target = live ? p.targets[t] - p.row0 : -1;
+  const float* y = p.y + static_cast<size_t>(t) * p.V;
+  uint16_t* G = p.G + static_cast<size_t>(t) * p.pitch;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kGPiece / 512; ++i) {
+    const int v = v0 + 512 * i + 2 * threadIdx.x;
+    if (v >= p.Vp) break;
+    float x[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[e] = live && v + e < p.V ? __expf(y[v + e] - lse) : 0.f;
+      sum += x[e];
+      if (live && v + e == target) x[e] -= 1.f;
+    }
+    constexpr float k = 1 << kGradScale;
+    *reinterpret_cast<uint32_t*>(G + v) = pack_half2(x[0] * k, x[1] * k);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) part[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += part[w];
+    p.ssum[static_cast<size_t>(blockIdx.x) * p.T + t] = s;
+  }
+}
+
+// dX = G W~ for up to 256 tokens, the packed rows dequantised on the way:
+// D[column of W~][token], A = the 64-row x 256-column tile of W~ as the
+// dequantising warps leave it in shared memory (rows of 64 columns, so
+// MN-major: the transpose costs nothing), B = 64 columns of G by TMA.  A CTA
+// owns `nb` column blocks of 256 (2 nb accumulators of N TMEM columns fill the
+// 512) and a range of vocabulary rows, writes one partial dX, and dx_kernel adds
+// the partials of a column's CTAs in order.
+//   warps 0-15  dequantise: set w / 8 takes every second tile; a warp one 16-row
+//               m-tile x 128 columns of it, its packed bytes loaded kGwAhead
+//               tiles early straight into registers (one 16-byte load per lane
+//               and 64 columns: nothing to copy, wait for or re-read).
+//   warp 16     TMA of G        warp 17  MMA
+// Afterwards warps 0-15 write the accumulators.
+constexpr int kGwWarps = 18, kGwStages = 4, kGwMaxN = 256, kGwAhead = 2;
+constexpr uint32_t kGwTile = 256 * 128;        // 64 rows x 256 columns of fp16
+constexpr uint32_t kGwGOff = kGwStages * kGwTile;
+constexpr uint32_t kGwSmemMax = 231424;        // 226 KB: with the 1 KB of alignment all a block may have
+
+struct GwParams {
+  DequantParams rows;
+  int32_t n_mtiles, nk;        // k-steps of 64 rows
+  int32_t T, N;                // tokens; rounded up to 16
+  int32_t nb, chunks;          // column blocks of 256 per CTA; 64-column chunks in all
+  int32_t full, s_full, s_last;   // groups of nb whole blocks; row splits of those and of the last group
+  int32_t gstages;
+  uint32_t g_bytes, bar_off;
+  float* dx;                   // [split][T][Kc]
+  size_t split_stride;
+  uint32_t* status;
+};
+
+// Packed bytes of one 64-column chunk, as one lane holds them.
+template <int GM>
+struct RawChunk {
+  uint4 c, x;                  // codes; fifth bits (core: x.x) or the second half (correction)
+  uint32_t s[1 << GM];         // scale pairs
+};
+
+template <int GM>
+__device__ __forceinline__ void load_chunk(const DequantParams& p, const uint8_t* blk, int ks, int lane, RawChunk<GM>& r) {
+  const int gr = lane >> 2;
+  if (ks < p.n_res) {
+    r.c = ldg128(blk + p.off_res + ks * kResChunkBytes + lane * 16);
+    const uint8_t* s = blk + p.off_sres + ((ks * 64) >> p.g_log2) * kSresGroupBytes + gr * 4;
+#pragma unroll
+    for (int g = 0; g < (1 << GM); ++g) r.s[g] = ldg32(s + g * kSresGroupBytes);
+  } else if (ks < p.n_res + p.n_L) {
+    const int c = ks - p.n_res;
+    r.c = ldg128(blk + p.off_Lnib + c * kLNibChunkBytes + lane * 16);
+    r.x.x = ldg32(blk + p.off_Lhi + c * kLHiChunkBytes + lane * 4);
+    r.s[0] = ldg32(blk + p.off_sL + gr * 4);
+  } else {
+    const int c = 2 * (ks - p.n_res - p.n_L);
+    r.c = ldg128(blk + p.off_A + c * kAChunkBytes + lane * 16);
+    if (c + 1 < p.n_A) r.x = ldg128(blk + p.off_A + (c + 1) * kAChunkBytes + lane * 16);
+    r.s[0] = ldg32(blk + p.off_sA + gr * 4);
+  }
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// A chunk's 16 rows x 64 columns into the swizzled tile: lane (gr, cc) holds 16
+// columns of rows gr and gr + 8, stored as columns 16 cc .. 16 cc + 15 (32
+// contiguous bytes of each row; the order is undone when dX is written).
+template <int GM>
+__device__ __forceinline__ void store_chunk(const DequantParams& p, const RawChunk<GM>& r, int ks, uint32_t lo, uint32_t hi) {
+  uint32_t a[4][4], s0[4], s1[4];
+  if (ks < p.n_res) {
+    const uint32_t w[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      unpack_int4_signed(w[st], a[st]);
+      if (st % (4 >> GM) == 0) scales_of(r.s[st >> (2 - GM)], p.sc_res, s0[st], s1[st]);
+      else s0[st] = s0[st - 1], s1[st] = s1[st - 1];
+    }
+  } else {
+    if (ks < p.n_res + p.n_L) {
+      unpack_int5_signed<0>(r.c.x, r.x.x, a[0]);
+      unpack_int5_signed<1>(r.c.y, r.x.x, a[1]);
+      unpack_int5_signed<2>(r.c.z, r.x.x, a[2]);
+      unpack_int5_signed<3>(r.c.w, r.x.x, a[3]);
+      scales_of(r.s[0], p.sc_L, s0[0], s1[0]);
+    } else {
+      unpack_int8_signed(r.c.x, r.c.y, a[0]);
+      unpack_int8_signed(r.c.z, r.c.w, a[1]);
+      if (2 * (ks - p.n_res - p.n_L) + 1 < p.n_A) {
+        unpack_int8_signed(r.x.x, r.x.y, a[2]);
+        unpack_int8_signed(r.x.z, r.x.w, a[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[2][i] = a[3][i] = 0u;
+      }
+      scales_of(r.s[0], p.sc_A, s0[0], s1[0]);
+    }
+#pragma unroll
+    for (int st = 1; st < 4; ++st) s0[st] = s0[0], s1[st] = s1[0];
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t at = h ? hi : lo;
+    const int i = 2 * h, j = 2 * h + 1;
+    sts128(at, hmul2_bits(a[i][0], s0[i]), hmul2_bits(a[i][2], s0[i]), hmul2_bits(a[j][0], s0[j]), hmul2_bits(a[j][2], s0[j]));
+    sts128(at + 1024u, hmul2_bits(a[i][1], s1[i]), hmul2_bits(a[i][3], s1[i]), hmul2_bits(a[j][1], s1[j]),
+           hmul2_bits(a[j][3], s1[j]));
+  }
+}
+
+template <int GM>
+__global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p, const __grid_constant__ CUtensorMap mg) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t tiles = smem_addr(base), gtiles = tiles + kGwGOff;
+  const uint32_t wfull = tiles + p.bar_off, wempty = wfull + 8 * kGwStages, gfull = wempty + 8 * kGwStages,
+                 gempty = gfull + 32, done = gempty + 32;
+  uint32_t* tmem = reinterpret_cast<uint32_t*>(base + p.bar_off + 16 * kGwStages + 72);
+  int* flag = reinterpret_cast<int*>(tmem + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGwStages; ++s) {
+      mbar_init(wfull + 8 * s, 8);
+      mbar_init(wempty + 8 * s, 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(gfull + 8 * s, 1);
+      mbar_init(gempty + 8 * s, 1);
+    }
+    mbar_init(done, 1);
+    *flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 17) {
+    tmem_alloc(smem_addr(tmem), kGTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem;
+
+  // This CTA: column group, its chunks and blocks, its k-steps.
+  const int u = blockIdx.x;
+  const bool whole = u < p.full * p.s_full;
+  const int group = whole ? u / p.s_full : p.full;
+  const int split = whole ? u - group * p.s_full : u - p.full * p.s_full, splits = whole ? p.s_full : p.s_last;
+  const int c0 = group * p.nb * 4, nc = min(4 * p.nb, p.chunks - c0), nbl = (nc + 3) / 4;
+  const int k0 = static_cast<int>(static_cast<int64_t>(p.nk) * split / splits);
+  const int k1 = static_cast<int>(static_cast<int64_t>(p.nk) * (split + 1) / splits);
+
+  if (warp < 16) {
+    const int set = warp >> 3, j = warp & 3, half = (warp >> 2) & 1, total = (k1 - k0) * nbl;
+    const int gr = lane >> 2, cc = lane & 3;
+    // byte offsets of this lane inside a tile: row 16 j + gr, 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
+    const uint32_t row = static_cast<uint32_t>((16 * j + gr) * 128) + half * 16384u;
+    const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16), o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
+    RawChunk<GM> raw[kGwAhead][2];
+    int pit = set, pk = k0 + set / nbl, pb = set % nbl;   // the tile to load next
+    auto load = [&](RawChunk<GM> (&r)[2]) {
+      const int mt = 4 * pk + j, c = 4 * pb + 2 * half;
+      if (pit < total && mt < p.n_mtiles) {
+        const uint8_t* blk = p.rows.mtiles + static_cast<size_t>(mt) * p.rows.mblk_bytes;
+        if (c < nc) load_chunk<GM>(p.rows, blk, c0 + c, lane, r[0]);
+        if (c + 1 < nc) load_chunk<GM>(p.rows, blk, c0 + c + 1, lane, r[1]);
+      }
+      pit += 2;
+      pb += 2;
+      while (pb >= nbl) {
+        pb -= nbl;
+        ++pk;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kGwAhead; ++i) load(raw[i]);
+    int k = k0 + set / nbl, b = set % nbl;
+    bool ok = true;
+    for (int it = set; it < total && ok;) {
+#pragma unroll
+      for (int i = 0; i < kGwAhead; ++i) {
+        if (it >= total || !ok) break;
+        const int s = it & (kGwStages - 1), c = 4 * b + 2 * half;
+        ok = warp_wait(flag, wempty + 8 * s, ((it / kGwStages) & 1) ^ 1, p.status);
+        if (!ok) break;
+        const uint32_t tile = tiles + s * kGwTile;
+        if (4 * k + j < p.n_mtiles) {
+          if (c < nc) store_chunk<GM>(p.rows, raw[i][0], c0 + c, tile + o_lo, tile + o_hi);
+          if (c + 1 < nc) store_chunk<GM>(p.rows, raw[i][1], c0 + c + 1, tile + o_lo + 8192u, tile + o_hi + 8192u);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            sts128(tile + o_lo + h * 8192u, 0u, 0u, 0u, 0u);
+            sts128(tile + o_lo + h * 8192u + 1024u, 0u, 0u, 0u, 0u);
+            sts128(tile + o_hi + h * 8192u, 0u, 0u, 0u, 0u);
+            sts128(tile + o_hi + h * 8192u + 1024u, 0u, 0u, 0u, 0u);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(wfull + 8 * s);
+        load(raw[i]);
+        it += 2;
+        b += 2;
+        while (b >= nbl) {
+          b -= nbl;
+          ++k;
+        }
+      }
+    }
+    // The accumulators: lane quarter w % 4 (columns of W~), every fourth block
+    // of 128 columns, 16 tokens at a time.
+    if (warp_wait(flag, done, 0u, p.status)) {
+      tc_fence_after();
+      const int q = warp & 3, m = 32 * q + lane, at = m & 63;
+      // the column's place in the operand order
+      const int pos = (m & 64) + ((at >> 2) & 3) * 16 + (at >> 4) * 4 + (at & 3);
+      float* dx = p.dx + split * p.split_stride + c0 * 64;
+      for (int blk = warp >> 2; 2 * blk < nc; blk += 4) {
+        for (int t0 = 0; t0 < p.T; t0 += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tbase + (static_cast<uint32_t>(32 * q) << 16) + blk * p.N + t0, r);
+          tmem_ld_wait();
+          if (2 * blk + (m >> 6) < nc) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (t0 + i < p.T) dx[static_cast<size_t>(t0 + i) * p.rows.Kc + blk * 128 + pos] = __uint_as_float(r[i]);
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp == 16) {
+    int issued = 0;
+    bool ok = true;
+    for (int k = k0; k < k1 && ok; ++k, ++issued) {
+      const int s = issued % p.gstages;
+      ok = warp_wait(flag, gempty + 8 * s, ((issued / p.gstages) & 1) ^ 1, p.status);
+      if (!ok) break;
+      if (elect_one()) {
+        mbar_arrive_expect_tx(gfull + 8 * s, p.g_bytes);
+        tma_load_2d(gtiles + s * p.g_bytes, &mg, k * 64, 0, gfull + 8 * s);
+      }
+      __syncwarp();
+    }
+    if (!ok) {
+      // Copies still in flight land before the block's shared memory goes away.
+      const int back = min(issued, p.gstages);
+      for (int i = 1; i <= back; ++i) mbar_wait(gfull + 8 * ((issued - i) % p.gstages), ((issued - i) / p.gstages) & 1u);
+    }
+  } else {
+    const uint32_t idesc = tc_idesc_f16(128, p.N) | kTcIdescAmn;
+    const uint64_t ad0 = smem_desc_mn128(tiles, 8192u), bd0 = smem_desc_k128(gtiles);
+    bool ok = true;
+    int it = 0;
+    for (int k = k0; k < k1 && ok; ++k) {
+      const int gs = (k - k0) % p.gstages;
+      ok = warp_wait(flag, gfull + 8 * gs, ((k - k0) / p.gstages) & 1, p.status);
+      if (!ok) break;
+      const uint64_t bd = bd0 + static_cast<uint64_t>(gs) * (p.g_bytes >> 4);
+      for (int b = 0; b < nbl; ++b, ++it) {
+        const int s = it & (kGwStages - 1);
+        ok = warp_wait(flag, wfull + 8 * s, (it / kGwStages) & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = ad0 + static_cast<uint64_t>(s) * (kGwTile >> 4);
+          const uint32_t d = tbase + 2 * b * p.N;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (4 * b + 2 * i < nc) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                tc_mma_ss(d + i * p.N, a + i * 1024 + e * 128, bd + 2 * e, idesc, (k != k0 || e != 0) ? 1u : 0u);
+            }
+          }
+          tc_commit(wempty + 8 * s);
+          if (b == nbl - 1) tc_commit(gempty + 8 * gs);
+        }
+        __syncwarp();
+      }
+    }
+    if (ok && elect_one()) tc_commit(done);
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tbase, kGTmem);
+  }
+}
+
 // -------------------------------------------------------------------- host
+constexpr int kFewTokens = 128;   // up to here the packed rows are dequantised inside the second product
+
+// Work split of gw_kernel.
+struct GwPlan {
+  int N, nb, chunks, full, s_full, s_last, nk;
+};
+GwPlan gw_plan(const archead_handle& h, int T) {
+  GwPlan g{};
+  g.N = (T + 15) / 16 * 16;
+  g.chunks = tc_kc(h.L) / 64;
+  g.nk = (h.L.n_mtiles + 3) / 4;
+  // As many column blocks as the TMEM holds (G is read once per group), fewer
+  // where the head is too small to give every SM a few tiles.
+  for (g.nb = kGwMaxN / g.N; g.nb > 1; --g.nb)
+    if (static_cast<int64_t>((g.chunks + 4 * g.nb - 1) / (4 * g.nb)) * g.nk >= 8 * h.num_sms) break;
+  g.full = g.chunks / (4 * g.nb);
+  const int rest = g.chunks - g.full * 4 * g.nb;
+  const auto share = [&](int c) {
+    return std::max(1, std::min(g.nk, static_cast<int>(static_cast<int64_t>(h.num_sms) * c / g.chunks)));
+  };
+  g.s_full = g.full > 0 ? share(4 * g.nb) : 0;
+  g.s_last = rest > 0 ? share(rest) : 0;
+  return g;
+}
+
 struct GradLayout {
-  int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; K splits of the accumulation
-  size_t cinv, ssum, xop, w, g, dx, dz, rb, escale, zhi, zlo, total;
+  bool few;
+  int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
+  int pitch, n_ssum;
+  size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, escale, zhi, zlo, total;
 };
 
 GradLayout grad_layout(const archead_handle& h, int T) {
   const Layout& L = h.L;
   GradLayout o{};
-  o.tokens = std::min(T, kGradTokens);
-  const int n_chunks = (L.Vp + kGradChunk - 1) / kGradChunk;
-  o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
   const int Kc = tc_kc(L);
   o.Kz = Kc - L.d;
-  // Few tiles: the accumulation splits its K (the rows of a chunk) so that
-  // every SM has a unit; the splits are added in order at the end.
-  const int tiles = ((o.tokens + kGM - 1) / kGM) * ((Kc + kGN - 1) / kGN);
-  o.splits = std::max(1, std::min(h.num_sms / tiles, o.chunk / 256));
-  const size_t t = o.tokens;
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t r = at;
     at += round_up(bytes, 256);
     return r;
   };
-  o.cinv = take(t * 4);
-  o.ssum = take((L.Vp + kGN - 1) / kGN * t * 4);
-  o.xop = take(t * Kc * 2);
-  o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
-  o.g = take(t * o.chunk * 2);
+  o.few = T <= kFewTokens;
+  const size_t t = o.few ? T : std::min(T, kGradTokens);
+  o.tokens = static_cast<int>(t);
+  if (o.few) {
+    // The forward call's workspace comes first: its header is this one's.
+    o.fwd = ws_layout(h, T).total;
+    at = round_up(o.fwd, 256);
+    o.pitch = static_cast<int>(round_up(L.Vp, 64));
+    o.n_ssum = (L.Vp + kGPiece - 1) / kGPiece;
+    o.logits = take(t * L.V * 4);
+    const GwPlan g = gw_plan(h, T);
+    o.splits = std::max(g.s_full, g.s_last);
+  } else {
+    const int n_chunks = (L.Vp + kGradChunk - 1) / kGradChunk;
+    o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
+    o.pitch = o.chunk;
+    o.n_ssum = (L.Vp + kGN - 1) / kGN;
+    // Few tiles: the accumulation splits its K (the rows of a chunk) so that
+    // every SM has a unit; the splits are added in order at the end.
+    const int tiles = ((o.tokens + kGM - 1) / kGM) * ((Kc + kGN - 1) / kGN);
+    o.splits = std::max(1, std::min(h.num_sms / tiles, o.chunk / 256));
+    o.cinv = take(t * 4);
+    o.xop = take(t * Kc * 2);
+    o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
+  }
+  o.ssum = take(o.n_ssum * t * 4);
+  o.g = take(t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
   o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
-  if (!h.tc_ok) {
+  if (!o.few && !h.tc_ok) {
     o.escale = take(t * 4);
     o.zhi = take(t * L.Kz * 2);
     o.zlo = take(t * L.Kz * 2);
@@ -698,38 +1085,16 @@ cudaError_t grad_activations(const archead_handle& h, const GradLayout& o, const
   return cudaGetLastError();
 }
 
-cudaError_t grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T,
-                        const int32_t* targets, const float* lse, const float* grad, void* out, bool out_f32,
-                        uint8_t* wb, cudaStream_t stream) {
+DequantParams dequant_params(const archead_handle& h, uint16_t* out) {
   const Layout& L = h.L;
-  const int Kc = tc_kc(L), Kz = o.Kz;
-  uint16_t* w = reinterpret_cast<uint16_t*>(wb + o.w);
-  uint16_t* rb = reinterpret_cast<uint16_t*>(wb + o.rb);
-  // Exponents of the last product: dz carries 2^beta (2^gamma), the rows of R
-  // (B) 2^rho, and both segments meet in one accumulator.
-  int sigma = L.r_c > 0 ? h.tc_beta + h.tc_rho_c : 1 << 20;
-  if (L.r_r > 0) sigma = std::min(sigma, h.tc_gamma + h.tc_rho_r);
-  if (Kz == 0) sigma = 0;
-  // The header: status word, tickets of the activation kernel.
-  cudaError_t e = cudaMemsetAsync(wb, 0, 256, stream);
-  if (e != cudaSuccess) return e;
-  if (Kz > 0) {
-    LowrankParams lp{reinterpret_cast<const int8_t*>(h.arena + L.off_R),
-                     reinterpret_cast<const uint16_t*>(h.arena + L.off_sR),
-                     reinterpret_cast<const int8_t*>(h.arena + L.off_B),
-                     reinterpret_cast<const uint16_t*>(h.arena + L.off_sB), rb, L.d, L.rcp, L.rrp, Kz, L.g_B,
-                     std::ldexp(1.f, sigma - h.tc_beta), std::ldexp(1.f, sigma - h.tc_gamma)};
-    lowrank_rows_kernel<<<Kz, 256, 0, stream>>>(lp);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
   DequantParams dq{};
   dq.mtiles = h.arena;
-  dq.out = w;
-  dq.Kc = Kc;
+  dq.out = out;
+  dq.Kc = tc_kc(L);
   dq.n_res = L.n_res;
   dq.n_L = L.n_L;
   dq.n_A = L.n_A;
-  dq.n_ks = Kc / 64;
+  dq.n_ks = dq.Kc / 64;
   while ((1 << dq.g_log2) < L.g) ++dq.g_log2;
   dq.off_res = L.off_res;
   dq.off_Lnib = L.off_Lnib;
@@ -742,10 +1107,153 @@ cudaError_t grad_launch(const archead_handle& h, const GradLayout& o, const uint
   dq.sc_res = std::ldexp(1.f, h.tc_alpha);
   dq.sc_L = std::ldexp(1.f, h.tc_beta);
   dq.sc_A = std::ldexp(1.f, h.tc_gamma);
-  for (int t0 = 0; t0 < T; t0 += o.tokens) {
+  return dq;
+}
+
+struct GradCall {
+  const archead_handle& h;
+  const GradLayout& o;
+  uint8_t* wb;
+  cudaStream_t stream;
+  int sigma;                  // dz carries 2^beta (2^gamma), the rows of R (B) 2^rho: both meet in 2^sigma
+};
+
+// The rows of R and B for the last product.
+int grad_lowrank(const GradCall& c) {
+  const Layout& L = c.h.L;
+  if (c.o.Kz == 0) return ARCHEAD_OK;
+  LowrankParams lp{reinterpret_cast<const int8_t*>(c.h.arena + L.off_R),
+                   reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sR),
+                   reinterpret_cast<const int8_t*>(c.h.arena + L.off_B),
+                   reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sB),
+                   reinterpret_cast<uint16_t*>(c.wb + c.o.rb), L.d, L.rcp, L.rrp, c.o.Kz, L.g_B,
+                   std::ldexp(1.f, c.sigma - c.h.tc_beta), std::ldexp(1.f, c.sigma - c.h.tc_gamma)};
+  lowrank_rows_kernel<<<c.o.Kz, 256, 0, c.stream>>>(lp);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
+}
+
+// dX -> dh of one pass's tokens.
+int grad_finish(const GradCall& c, GemmParams& p, int splits, int splits_last, int last) {
+  const Layout& L = c.h.L;
+  const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
+  uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
+  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, c.o.n_ssum, nt, Kc, L.d,
+              L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, splits_last, last};
+  dx_kernel<<<dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream>>>(dp);
+  cudaError_t e = cudaGetLastError();
+  CUtensorMap mz{}, mr{};
+  if (e == cudaSuccess && Kz > 0) {
+    e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM);
+    if (e == cudaSuccess) e = tc_encode_map(&mr, reinterpret_cast<const uint16_t*>(c.wb + c.o.rb), L.d, Kz, L.d, 64);
+  }
+  if (e != cudaSuccess) return set_cuda_error(e);
+  p.N = L.d;
+  p.n_k = Kz / 64;
+  p.splits = 1;
+  p.mul_acc = std::ldexp(1.f, -c.sigma);
+  p.mul_dx = std::ldexp(1.f, -kGradScale - c.h.tc_alpha);
+  e = launch_gemm<kFinish>(p, mz, mr, c.h.num_sms, c.stream);
+  return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
+}
+
+// Few tokens: the forward kernels' logits, G, then G W~ from the packed rows.
+int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
+  const archead_handle& h = c.h;
+  const Layout& L = h.L;
+  const int T = p.M;
+  float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
+  const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
+  if (rc != ARCHEAD_OK) return rc;
+  GParams gp{logits, p.lse, p.grad, p.targets, p.G, p.ssum, T, L.V, L.Vp, h.row0, c.o.pitch};
+  g_kernel<<<dim3(c.o.n_ssum, T), 256, 0, c.stream>>>(gp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return set_cuda_error(e);
+  const GwPlan g = gw_plan(h, T);
+  GwParams w{};
+  w.rows = dequant_params(h, nullptr);
+  w.n_mtiles = L.n_mtiles;
+  w.nk = g.nk;
+  w.T = T;
+  w.N = g.N;
+  w.nb = g.nb;
+  w.chunks = g.chunks;
+  w.full = g.full;
+  w.s_full = g.s_full;
+  w.s_last = g.s_last;
+  w.g_bytes = static_cast<uint32_t>(g.N) * 128u;
+  w.gstages = static_cast<int>(std::min<uint32_t>(4, (kGwSmemMax - kGwGOff - 256) / w.g_bytes));
+  w.bar_off = kGwGOff + w.gstages * w.g_bytes;
+  w.dx = p.dx;
+  w.split_stride = p.split_stride;
+  w.status = p.status;
+  CUtensorMap mg;
+  e = tc_encode_map(&mg, p.G, L.Vp, T, c.o.pitch, g.N);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  const int grid = g.full * g.s_full + g.s_last;
+  const uint32_t smem = w.bar_off + 256 + 1024;
+  if (w.rows.g_log2 >= 6) gw_kernel<0><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
+  else if (w.rows.g_log2 == 5) gw_kernel<1><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
+  else gw_kernel<2><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return set_cuda_error(e);
+  return grad_finish(c, p, g.s_full, g.s_last, g.full * g.nb * 256);
+}
+
+// Many tokens: chunk by chunk through the dequantised rows.
+int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
+  const archead_handle& h = c.h;
+  const Layout& L = h.L;
+  const GradLayout& o = c.o;
+  const int Kc = tc_kc(L), nt = p.M;
+  uint16_t* w = reinterpret_cast<uint16_t*>(c.wb + o.w);
+  cudaError_t e = grad_activations(h, o, hidden, nt, c.wb, c.stream);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  DequantParams dq = dequant_params(h, w);
+  p.cinv = reinterpret_cast<const float*>(c.wb + o.cinv);
+  const uint16_t* xop = reinterpret_cast<const uint16_t*>(c.wb + o.xop);
+  CUtensorMap mx, mg, mwk, mwn;
+  for (int v0 = 0; v0 < L.Vp; v0 += o.chunk) {
+    const int rows = std::min(o.chunk, L.Vp - v0);
+    dq.mt0 = v0 / kMT;
+    dq.n_mt = rows / kMT;
+    const int64_t items = static_cast<int64_t>(dq.n_mt) * dq.n_ks;
+    dequant_rows_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, c.stream>>>(dq);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = tc_encode_map(&mx, xop, Kc, nt, Kc, kGM);
+    if (e == cudaSuccess) e = tc_encode_map(&mg, p.G, rows, nt, o.pitch, kGM);
+    if (e == cudaSuccess) e = tc_encode_map(&mwk, w, Kc, rows, Kc, kGN);
+    if (e == cudaSuccess) e = tc_encode_map(&mwn, w, Kc, rows, Kc, 64);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    p.v0 = v0;
+    p.N = rows;
+    p.n_k = Kc / 64;
+    p.splits = 1;
+    e = launch_gemm<kSoftmax>(p, mx, mwk, h.num_sms, c.stream);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    p.N = Kc;
+    p.n_k = (rows + 63) / 64;
+    p.splits = o.splits;
+    p.first = v0 == 0;
+    e = launch_gemm<kAccumulate>(p, mg, mwn, h.num_sms, c.stream);
+    if (e != cudaSuccess) return set_cuda_error(e);
+  }
+  return grad_finish(c, p, o.splits, o.splits, Kc);
+}
+
+int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T, const int32_t* targets,
+                const float* lse, const float* grad, void* out, bool out_f32, uint8_t* wb, cudaStream_t stream) {
+  const Layout& L = h.L;
+  GradCall c{h, o, wb, stream, L.r_c > 0 ? h.tc_beta + h.tc_rho_c : 1 << 20};
+  if (L.r_r > 0) c.sigma = std::min(c.sigma, h.tc_gamma + h.tc_rho_r);
+  if (o.Kz == 0) c.sigma = 0;
+  // The header: status word, tickets of the activation kernel.
+  const cudaError_t e = cudaMemsetAsync(wb, 0, 256, stream);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  int rc = grad_lowrank(c);
+  for (int t0 = 0; t0 < T && rc == ARCHEAD_OK; t0 += o.tokens) {
     const int nt = std::min(o.tokens, T - t0);
-    e = grad_activations(h, o, hidden + static_cast<size_t>(t0) * L.d, nt, wb, stream);
-    if (e != cudaSuccess) return e;
+    const size_t first = static_cast<size_t>(t0) * L.d;
     GemmParams p{};
     p.M = nt;
     p.status = reinterpret_cast<uint32_t*>(wb + 4);
@@ -753,66 +1261,20 @@ cudaError_t grad_launch(const archead_handle& h, const GradLayout& o, const uint
     p.targets = targets + t0;
     p.row0 = h.row0;
     p.v_total = h.v_total;
-    p.cinv = reinterpret_cast<const float*>(wb + o.cinv);
     p.lse = lse + t0;
     p.G = reinterpret_cast<uint16_t*>(wb + o.g);
-    p.pitch = o.chunk;
+    p.pitch = o.pitch;
     p.V = L.V;
-    p.dx = reinterpret_cast<float*>(wb + o.dx);
-    p.split_stride = static_cast<size_t>(nt) * Kc;
-    p.Kc = Kc;
     p.ssum = reinterpret_cast<float*>(wb + o.ssum);
     p.tokens = nt;
-    const uint16_t* xop = reinterpret_cast<const uint16_t*>(wb + o.xop);
-    CUtensorMap mx, mg, mwk, mwn;
-    for (int v0 = 0; v0 < L.Vp; v0 += o.chunk) {
-      const int rows = std::min(o.chunk, L.Vp - v0);
-      dq.mt0 = v0 / kMT;
-      dq.n_mt = rows / kMT;
-      const int64_t items = static_cast<int64_t>(dq.n_mt) * dq.n_ks;
-      dequant_rows_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, stream>>>(dq);
-      if ((e = cudaGetLastError()) != cudaSuccess) return e;
-      e = tc_encode_map(&mx, xop, Kc, nt, Kc, kGM);
-      if (e == cudaSuccess) e = tc_encode_map(&mg, p.G, rows, nt, o.chunk, kGM);
-      if (e == cudaSuccess) e = tc_encode_map(&mwk, w, Kc, rows, Kc, kGN);
-      if (e == cudaSuccess) e = tc_encode_map(&mwn, w, Kc, rows, Kc, 64);
-      if (e != cudaSuccess) return e;
-      p.v0 = v0;
-      p.N = rows;
-      p.n_k = Kc / 64;
-      p.splits = 1;
-      e = launch_gemm<kSoftmax>(p, mx, mwk, h.num_sms, stream);
-      if (e != cudaSuccess) return e;
-      p.N = Kc;
-      p.n_k = (rows + 63) / 64;
-      p.splits = o.splits;
-      p.first = v0 == 0;
-      e = launch_gemm<kAccumulate>(p, mg, mwn, h.num_sms, stream);
-      if (e != cudaSuccess) return e;
-    }
-    uint16_t* dz = reinterpret_cast<uint16_t*>(wb + o.dz);
-    DxParams dp{dq, p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, (L.Vp + kGN - 1) / kGN, nt, o.splits, Kc, L.d,
-                L.V, h.row0, h.v_total == L.V ? 1 : 0};
-    dx_kernel<<<nt, 256, 0, stream>>>(dp);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    CUtensorMap mz{}, mr{};
-    if (Kz > 0) {
-      e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM);
-      if (e == cudaSuccess) e = tc_encode_map(&mr, rb, L.d, Kz, L.d, 64);
-      if (e != cudaSuccess) return e;
-    }
-    p.N = L.d;
-    p.n_k = Kz / 64;
-    p.splits = 1;
-    p.out = out_f32 ? static_cast<void*>(static_cast<float*>(out) + static_cast<size_t>(t0) * L.d)
-                    : static_cast<void*>(static_cast<uint16_t*>(out) + static_cast<size_t>(t0) * L.d);
+    p.dx = reinterpret_cast<float*>(wb + o.dx);
+    p.Kc = tc_kc(L);
+    p.split_stride = static_cast<size_t>(nt) * p.Kc;
+    p.out = out_f32 ? static_cast<void*>(static_cast<float*>(out) + first) : static_cast<void*>(static_cast<uint16_t*>(out) + first);
     p.out_f32 = out_f32 ? 1 : 0;
-    p.mul_acc = std::ldexp(1.f, -sigma);
-    p.mul_dx = std::ldexp(1.f, -kGradScale - h.tc_alpha);
-    e = launch_gemm<kFinish>(p, mz, mr, h.num_sms, stream);
-    if (e != cudaSuccess) return e;
+    rc = o.few ? grad_few(c, hidden + first, p) : grad_many(c, hidden + first, p);
   }
-  return cudaSuccess;
+  return rc;
 }
 
 constexpr int kMaxTokens = 1 << 20;
@@ -825,6 +1287,9 @@ cudaError_t grad_set_attributes() {
     e = cudaFuncSetAttribute(grad_gemm_kernel<kAccumulate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(grad_gemm_kernel<kFinish>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+  for (const void* k : {reinterpret_cast<const void*>(&gw_kernel<0>), reinterpret_cast<const void*>(&gw_kernel<1>),
+                        reinterpret_cast<const void*>(&gw_kernel<2>)})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGwSmemMax + 1024);
   return e;
 }
 
@@ -856,7 +1321,6 @@ extern "C" ARCHEAD_API int archead_grad_hidden(const archead_handle* handle, con
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return set_cuda_error(e);
   if (dev != handle->device) return ARCHEAD_EINVAL;
-  e = grad_launch(*handle, o, hidden, T, targets, lse, grad_ce, grad_hidden, grad_dtype == ARCHEAD_GRAD_F32,
-                  static_cast<uint8_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
+  return grad_launch(*handle, o, hidden, T, targets, lse, grad_ce, grad_hidden, grad_dtype == ARCHEAD_GRAD_F32,
+                     static_cast<uint8_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
 }

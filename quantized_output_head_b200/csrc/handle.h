@@ -148,6 +148,10 @@ cudaError_t launch_tc_merge(const float4* partials, int n_mt128, int T, const in
 cudaError_t launch_shard_merge(const float4* parts, int n, int T, float* lse, int32_t* argmax, float* ce,
                                cudaStream_t stream);
 
+// Logits of the forward call (api.cu), without its profiling events.
+int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float* logits, void* ws, size_t ws_bytes,
+                   cudaStream_t stream);
+
 // Gradient of the head (grad.cu).
 cudaError_t grad_set_attributes();
 

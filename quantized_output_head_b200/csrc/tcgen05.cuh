@@ -80,8 +80,8 @@ __host__ __device__ constexpr uint32_t tc_idesc_f16(int M, int N) {
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
 
-// Bit of the instruction descriptor that makes B MN-major (stored [K][N]).
-constexpr uint32_t kTcIdescBmn = 1u << 16;
+// Bits of the instruction descriptor that make A (B) MN-major (stored [K][M or N]).
+constexpr uint32_t kTcIdescAmn = 1u << 15, kTcIdescBmn = 1u << 16;
 
 // Shared-memory matrix descriptor of a K-major operand tile stored with the
 // 128-byte swizzle: rows of 128 bytes (64 fp16), 8-row atoms of 1024 bytes.
