@@ -241,7 +241,7 @@ struct DxParams {
   size_t split_stride;
   uint16_t* dz;
   int32_t n_ssum, tokens, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
-  int32_t splits, splits_last, last;               // partial dX of columns below `last`, and of the rest
+  int32_t splits, splits_small, groups, big;       // partial dX of a block of 128 columns b: `splits` if b % groups < big
 };
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   __shared__ float part[8];
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   float* dx = p.dx + static_cast<size_t>(t) * p.Kc;
   for (int q = q0; q < p.Kc / 4; q += dq) {
     float4 v = reinterpret_cast<const float4*>(dx)[q];
-    const int n = 4 * q < p.last ? p.splits : p.splits_last;
+    const int n = (q / 32) % p.groups < p.big ? p.splits : p.splits_small;
     for (int s = 1; s < n; ++s) {
       const float4 x = reinterpret_cast<const float4*>(dx + s * p.split_stride)[q];
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
@@ -404,42 +404,65 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
   }
 }
 
+// The whole warp walks the k-steps and one elected lane issues.  Issuing a
+// tcgen05.mma costs mostly the instructions that prepare its operands, so each
+// is an immediate offset from running values that advance by constants.
 template <GemmMode kMode>
 __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base) {
   constexpr bool kMn = kMode != kSoftmax;
+  constexpr uint32_t kBStep = kMn ? 128u : 2u;   // descriptor units per K = 16
+  constexpr uint32_t kStep = kGStageBytes >> 4;
   const uint64_t ad0 = smem_desc_k128(sm.stages);
   const uint64_t bd0 = kMn ? smem_desc_mn128(sm.stages + kGABytes, 8192u) : smem_desc_k128(sm.stages + kGABytes);
-  constexpr uint32_t kBStep = kMn ? 128u : 2u;   // descriptor units per K = 16
-  int s = 0, i = 0;
-  uint32_t ph = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++i) {
+  uint64_t a = ad0, b = bd0;
+  uint32_t full = sm.full, empty = sm.empty, ph = 0, aph = 1, d = tmem_base, accf = sm.accf, acce = sm.acce;
+  int s = 0;
+  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const GemmUnit w = g_unit(p, u);
-    const uint32_t acc = i & 1;
-    if (!g_wait(sm, sm.acce + 8 * acc, ((i >> 1) & 1) ^ 1, p.status)) return;
+    if (!g_wait(sm, acce, aph, p.status)) return;
     tc_fence_after();
     const int ncol = (min(kGN, p.N - w.n * kGN) + 15) & ~15;
     const uint32_t idesc = tc_idesc_f16(kGM, ncol) | (kMn ? kTcIdescBmn : 0u);
-    const uint32_t d = tmem_base + acc * kGN;
+    uint32_t acc = 0;
     for (int k = w.k0; k < w.k1; ++k) {
-      if (!g_wait(sm, sm.full + 8 * s, ph, p.status)) return;
+      if (!g_wait(sm, full, ph, p.status)) return;
       tc_fence_after();
       if (elect_one()) {
-        const uint64_t a = ad0 + static_cast<uint64_t>(s) * (kGStageBytes >> 4);
-        const uint64_t b = bd0 + static_cast<uint64_t>(s) * (kGStageBytes >> 4);
-        tc_mma_ss(d, a, b, idesc, k != w.k0);
+        tc_mma_ss(d, a, b, idesc, acc);
         tc_mma_ss(d, a + 2, b + kBStep, idesc, 1u);
         tc_mma_ss(d, a + 4, b + 2 * kBStep, idesc, 1u);
         tc_mma_ss(d, a + 6, b + 3 * kBStep, idesc, 1u);
-        tc_commit(sm.empty + 8 * s);
+        tc_commit(empty);
       }
       __syncwarp();
+      acc = 1;
       if (++s == kGStages) {
         s = 0;
         ph ^= 1u;
+        a = ad0;
+        b = bd0;
+        full = sm.full;
+        empty = sm.empty;
+      } else {
+        a += kStep;
+        b += kStep;
+        full += 8;
+        empty += 8;
       }
     }
-    if (elect_one()) tc_commit(sm.accf + 8 * acc);
+    if (elect_one()) tc_commit(accf);
     __syncwarp();
+    // the other accumulator
+    if (d == tmem_base) {
+      d += kGN;
+      accf += 8;
+      acce += 8;
+    } else {
+      d = tmem_base;
+      accf = sm.accf;
+      acce = sm.acce;
+      aph ^= 1u;
+    }
   }
 }
 
@@ -618,111 +641,96 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
 }
 
 // ------------------------------------------------------- few tokens: G, G W~
-// G from the forward kernels' logits (fp32 [T][V]): one block per (token, piece
-// of kGPiece rows), with the piece's sum of exp(y - lse).
-constexpr int kGPiece = 2048;
+// G from the forward kernels' logits (fp32 [T][V]), in the order gw_kernel loads
+// it: pieces of 32 tokens x 128 rows of the head (8 KB), in a piece 16-byte runs
+// of 8 rows, the 32 tokens of a run side by side, so that a warp's load of one
+// run per lane (= token) is 512 contiguous bytes.  (Read row by row, 16 bytes of
+// 32 rows per load, G cost gw_kernel 37 of 161 us at 64 tokens.)  One block per
+// piece, with its tokens' sums of exp(y - lse).
 struct GParams {
   const float* y;
   const float* lse;
   const float* grad;
   const int32_t* targets;
-  uint16_t* G;                // [T][pitch]
-  float* ssum;                // [pieces][T]
-  int32_t T, V, Vp, row0, pitch;
+  uint4* G;                   // [k-step][T / 32][16][32]
+  float* ssum;                // [k-step][T]
+  int32_t T, V, row0;
 };
+constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
 __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
-  __shared__ float part[8];
-  const int t = blockIdx.y, v0 = blockIdx.x * kGPiece, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool live = p.grad[t] != 0.f;   // (its lse and target may be anything otherwise)
-  const float lse = live ? p.lse[t] : 0.f;
-  const int target = live ? p.targets[t] - p.row0 : -1;
-  const float* y = p.y + static_cast<size_t>(t) * p.V;
-  uint16_t* G = p.G + static_cast<size_t>(t) * p.pitch;
-  float sum = 0.f;
+  __shared__ __align__(16) uint16_t piece[kGwRows / 8][32][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = blockIdx.x * kGwRows;
 #pragma unroll
-  for (int i = 0; i < kGPiece / 512; ++i) {
-    const int v = v0 + 512 * i + 2 * threadIdx.x;
-    if (v >= p.Vp) break;
-    float x[2];
+  for (int i = 0; i < 4; ++i) {
+    const int tl = 4 * warp + i, t = 32 * blockIdx.y + tl;
+    const bool live = t < p.T && p.grad[t] != 0.f;   // (its lse and target may be anything otherwise)
+    const float lse = live ? p.lse[t] : 0.f;
+    const int target = live ? p.targets[t] - p.row0 : -1;
+    const float* y = p.y + static_cast<size_t>(t) * p.V;
+    float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      x[e] = live && v + e < p.V ? __expf(y[v + e] - lse) : 0.f;
-      sum += x[e];
-      if (live && v + e == target) x[e] -= 1.f;
+    for (int e = 0; e < kGwRows / 32; ++e) {
+      const int v = v0 + 32 * e + lane;
+      float x = live && v < p.V ? __expf(y[v] - lse) : 0.f;
+      sum += x;
+      if (live && v == target) x -= 1.f;
+      piece[4 * e + (lane >> 3)][tl][lane & 7] = __half_as_ushort(__float2half_rn(x * static_cast<float>(1 << kGradScale)));
     }
-    constexpr float k = 1 << kGradScale;
-    *reinterpret_cast<uint32_t*>(G + v) = pack_half2(x[0] * k, x[1] * k);
-  }
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) part[warp] = sum;
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0 && t < p.T) p.ssum[static_cast<size_t>(blockIdx.x) * p.T + t] = sum;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w];
-    p.ssum[static_cast<size_t>(blockIdx.x) * p.T + t] = s;
-  }
+  uint4* dst = p.G + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * (kGwRows / 8 * 32);
+  for (int i = threadIdx.x; i < kGwRows / 8 * 32; i += blockDim.x) dst[i] = reinterpret_cast<const uint4*>(piece)[i];
 }
 
-// dX = G W~ for up to 256 tokens, the packed rows dequantised on the way:
-// D[column of W~][token], A = the 64-row x 256-column tile of W~ as the
-// dequantising warps leave it in shared memory (rows of 64 columns, so
-// MN-major: the transpose costs nothing), B = 64 columns of G by TMA.  A CTA
-// owns `nb` column blocks of 256 (2 nb accumulators of N TMEM columns fill the
-// 512) and a range of vocabulary rows, writes one partial dX, and dx_kernel adds
-// the partials of a column's CTAs in order.
-//   warps 0-15  dequantise: set w / 8 takes every second tile; a warp one 16-row
-//               m-tile x 128 columns of it, its packed bytes loaded kGwAhead
-//               tiles early straight into registers (one 16-byte load per lane
-//               and 64 columns: nothing to copy, wait for or re-read).
-//   warp 16     TMA of G        warp 17  MMA
+// dX = G W~ for up to 128 tokens, the packed rows dequantised on the way:
+// D[128 tokens x 128 columns of W~] per accumulator, A = 128 columns of G in
+// TMEM, B = a 128-row x 128-column tile of W~ as the dequantising warps leave it
+// in shared memory (rows of 64 columns, so MN-major: the transpose costs
+// nothing).  The MMA reads its shared-memory operands at about 64 bytes a
+// clock, so with G there too a tile took nearly twice its clocks of math; and a
+// barrier round (wait, fence, commit) costs the MMA warp and the dequantising
+// warps some 250 clocks each whatever the tile, so tiles of 64 rows were bound
+// by that.  A CTA owns up to three column blocks (three accumulators and two
+// buffers of G fill the 512 TMEM columns) and a range of vocabulary rows, writes
+// one partial dX, and dx_kernel adds the partials of a column's CTAs in order.
+//   warps 0-15  dequantise: set w / 4 takes every fourth tile, a warp two 16-row
+//               m-tiles of it, their packed bytes loaded one of its tiles
+//               early straight into registers (one 16-byte load per lane and 64
+//               columns: nothing to copy, wait for or re-read).  They also bring
+//               G: warp w the 32 tokens of its TMEM lane quarter w % 4, 32
+//               columns of each k-step.
+//   warp 16     MMA
 // Afterwards warps 0-15 write the accumulators.
-constexpr int kGwWarps = 18, kGwStages = 4, kGwMaxN = 256, kGwAhead = 2;
-constexpr uint32_t kGwTile = 256 * 128;        // 64 rows x 256 columns of fp16
-constexpr uint32_t kGwGOff = kGwStages * kGwTile;
-constexpr uint32_t kGwSmemMax = 231424;        // 226 KB: with the 1 KB of alignment all a block may have
+constexpr int kGwWarps = 17, kGwSets = 4, kGwStages = 6, kGwBlocks = 3, kGwBufs = 2;
+constexpr uint32_t kGwHalf = kGwRows * 128;           // 128 rows x 64 columns of fp16
+constexpr uint32_t kGwTile = 2 * kGwHalf;
+constexpr uint32_t kGwBarOff = kGwStages * kGwTile;
+constexpr uint32_t kGwSmem = kGwBarOff + 512 + 1024;
 
 struct GwParams {
   DequantParams rows;
-  int32_t n_mtiles, nk;        // k-steps of 64 rows
-  int32_t T, N;                // tokens; rounded up to 16
-  int32_t nb, chunks;          // column blocks of 256 per CTA; 64-column chunks in all
-  int32_t full, s_full, s_last;   // groups of nb whole blocks; row splits of those and of the last group
-  int32_t gstages;
-  uint32_t g_bytes, bar_off;
+  const uint4* G;              // in g_kernel's order, zeros past the last row of the head
+  int32_t T;
+  int32_t n_mtiles, nk;        // k-steps of kGwRows rows
+  int32_t chunks;              // 64-column chunks in all
+  int32_t groups, big, s_big, s_small;   // group g: column blocks g, g + groups, ...; row splits of the first `big`, the others
   float* dx;                   // [split][T][Kc]
   size_t split_stride;
   uint32_t* status;
 };
 
-// Packed bytes of one 64-column chunk, as one lane holds them.
-template <int GM>
-struct RawChunk {
-  uint4 c, x;                  // codes; fifth bits (core: x.x) or the second half (correction)
-  uint32_t s[1 << GM];         // scale pairs
+// Packed bytes of two 64-column chunks of one m-tile, as one lane holds them:
+// codes; fifth bits (core: x.x) or the second half (correction); scale pairs.
+// GP: scale groups per 128 residual columns (8, 4, 2; 1 for groups of 128 and more).
+template <int GP>
+struct RawPair {
+  static constexpr int kPer = GP < 2 ? 1 : GP / 2;   // groups per chunk
+  uint4 c[2], x[2];
+  uint32_t s[2 * kPer];
 };
-
-template <int GM>
-__device__ __forceinline__ void load_chunk(const DequantParams& p, const uint8_t* blk, int ks, int lane, RawChunk<GM>& r) {
-  const int gr = lane >> 2;
-  if (ks < p.n_res) {
-    r.c = ldg128(blk + p.off_res + ks * kResChunkBytes + lane * 16);
-    const uint8_t* s = blk + p.off_sres + ((ks * 64) >> p.g_log2) * kSresGroupBytes + gr * 4;
-#pragma unroll
-    for (int g = 0; g < (1 << GM); ++g) r.s[g] = ldg32(s + g * kSresGroupBytes);
-  } else if (ks < p.n_res + p.n_L) {
-    const int c = ks - p.n_res;
-    r.c = ldg128(blk + p.off_Lnib + c * kLNibChunkBytes + lane * 16);
-    r.x.x = ldg32(blk + p.off_Lhi + c * kLHiChunkBytes + lane * 4);
-    r.s[0] = ldg32(blk + p.off_sL + gr * 4);
-  } else {
-    const int c = 2 * (ks - p.n_res - p.n_L);
-    r.c = ldg128(blk + p.off_A + c * kAChunkBytes + lane * 16);
-    if (c + 1 < p.n_A) r.x = ldg128(blk + p.off_A + (c + 1) * kAChunkBytes + lane * 16);
-    r.s[0] = ldg32(blk + p.off_sA + gr * 4);
-  }
-}
 
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -731,42 +739,43 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // A chunk's 16 rows x 64 columns into the swizzled tile: lane (gr, cc) holds 16
 // columns of rows gr and gr + 8, stored as columns 16 cc .. 16 cc + 15 (32
 // contiguous bytes of each row; the order is undone when dX is written).
-template <int GM>
-__device__ __forceinline__ void store_chunk(const DequantParams& p, const RawChunk<GM>& r, int ks, uint32_t lo, uint32_t hi) {
+template <int GP>
+__device__ __forceinline__ void store_chunk(const DequantParams& p, const RawPair<GP>& r, int ks, int ch, uint32_t lo, uint32_t hi) {
+  constexpr int kPer = RawPair<GP>::kPer;
   uint32_t a[4][4], s0[4], s1[4];
   if (ks < p.n_res) {
-    const uint32_t w[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+    const uint32_t w[4] = {r.c[ch].x, r.c[ch].y, r.c[ch].z, r.c[ch].w};
 #pragma unroll
     for (int st = 0; st < 4; ++st) {
       unpack_int4_signed(w[st], a[st]);
-      if (st % (4 >> GM) == 0) scales_of(r.s[st >> (2 - GM)], p.sc_res, s0[st], s1[st]);
+      if (st % (4 / kPer) == 0) scales_of(r.s[ch * kPer + st * kPer / 4], p.sc_res, s0[st], s1[st]);
       else s0[st] = s0[st - 1], s1[st] = s1[st - 1];
     }
   } else {
     if (ks < p.n_res + p.n_L) {
-      unpack_int5_signed<0>(r.c.x, r.x.x, a[0]);
-      unpack_int5_signed<1>(r.c.y, r.x.x, a[1]);
-      unpack_int5_signed<2>(r.c.z, r.x.x, a[2]);
-      unpack_int5_signed<3>(r.c.w, r.x.x, a[3]);
-      scales_of(r.s[0], p.sc_L, s0[0], s1[0]);
+      unpack_int5_signed<0>(r.c[ch].x, r.x[ch].x, a[0]);
+      unpack_int5_signed<1>(r.c[ch].y, r.x[ch].x, a[1]);
+      unpack_int5_signed<2>(r.c[ch].z, r.x[ch].x, a[2]);
+      unpack_int5_signed<3>(r.c[ch].w, r.x[ch].x, a[3]);
+      scales_of(r.s[ch * kPer], p.sc_L, s0[0], s1[0]);
     } else {
-      unpack_int8_signed(r.c.x, r.c.y, a[0]);
-      unpack_int8_signed(r.c.z, r.c.w, a[1]);
+      unpack_int8_signed(r.c[ch].x, r.c[ch].y, a[0]);
+      unpack_int8_signed(r.c[ch].z, r.c[ch].w, a[1]);
       if (2 * (ks - p.n_res - p.n_L) + 1 < p.n_A) {
-        unpack_int8_signed(r.x.x, r.x.y, a[2]);
-        unpack_int8_signed(r.x.z, r.x.w, a[3]);
+        unpack_int8_signed(r.x[ch].x, r.x[ch].y, a[2]);
+        unpack_int8_signed(r.x[ch].z, r.x[ch].w, a[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[2][i] = a[3][i] = 0u;
       }
-      scales_of(r.s[0], p.sc_A, s0[0], s1[0]);
+      scales_of(r.s[ch * kPer], p.sc_A, s0[0], s1[0]);
     }
 #pragma unroll
     for (int st = 1; st < 4; ++st) s0[st] = s0[0], s1[st] = s1[0];
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t at = h ? hi : lo;
+    const uint32_t at = (h ? hi : lo) + ch * kGwHalf;
     const int i = 2 * h, j = 2 * h + 1;
     sts128(at, hmul2_bits(a[i][0], s0[i]), hmul2_bits(a[i][2], s0[i]), hmul2_bits(a[j][0], s0[j]), hmul2_bits(a[j][2], s0[j]));
     sts128(at + 1024u, hmul2_bits(a[i][1], s1[i]), hmul2_bits(a[i][3], s1[i]), hmul2_bits(a[j][1], s1[j]),
@@ -774,30 +783,58 @@ __device__ __forceinline__ void store_chunk(const DequantParams& p, const RawChu
   }
 }
 
-template <int GM>
-__global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p, const __grid_constant__ CUtensorMap mg) {
+// The common case, both chunks residual.
+template <int GP>
+__device__ __forceinline__ void store_pair(const RawPair<GP>& r, float sc, uint32_t lo, uint32_t hi) {
+  uint32_t s0 = 0, s1 = 0;
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch) {
+    const uint32_t w[4] = {r.c[ch].x, r.c[ch].y, r.c[ch].z, r.c[ch].w};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t up[4], dn[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int st = 2 * h + e, step = 4 * ch + st;
+        if (step * GP % 8 == 0) scales_of(r.s[GP < 2 ? 0 : step * GP / 8], sc, s0, s1);
+        uint32_t a[4];
+        unpack_int4_signed(w[st], a);
+        up[2 * e] = hmul2_bits(a[0], s0);
+        up[2 * e + 1] = hmul2_bits(a[2], s0);
+        dn[2 * e] = hmul2_bits(a[1], s1);
+        dn[2 * e + 1] = hmul2_bits(a[3], s1);
+      }
+      const uint32_t at = (h ? hi : lo) + ch * kGwHalf;
+      sts128(at, up[0], up[1], up[2], up[3]);
+      sts128(at + 1024u, dn[0], dn[1], dn[2], dn[3]);
+    }
+  }
+}
+
+template <int GP>
+__global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t tiles = smem_addr(base), gtiles = tiles + kGwGOff;
-  const uint32_t wfull = tiles + p.bar_off, wempty = wfull + 8 * kGwStages, gfull = wempty + 8 * kGwStages,
-                 gempty = gfull + 32, done = gempty + 32;
-  uint32_t* tmem = reinterpret_cast<uint32_t*>(base + p.bar_off + 16 * kGwStages + 72);
+  const uint32_t tiles = smem_addr(base);
+  const uint32_t wfull = tiles + kGwBarOff, wempty = wfull + 8 * kGwStages, gfull = wempty + 8 * kGwStages,
+                 gempty = gfull + 8 * kGwBufs, done = gempty + 8 * kGwBufs;
+  uint32_t* tmem = reinterpret_cast<uint32_t*>(base + kGwBarOff + 16 * kGwStages + 16 * kGwBufs + 8);
   int* flag = reinterpret_cast<int*>(tmem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGwStages; ++s) {
-      mbar_init(wfull + 8 * s, 8);
+      mbar_init(wfull + 8 * s, 4);
       mbar_init(wempty + 8 * s, 1);
     }
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(gfull + 8 * s, 1);
+    for (int s = 0; s < kGwBufs; ++s) {
+      mbar_init(gfull + 8 * s, 4 * ((p.T + 31) / 32));
       mbar_init(gempty + 8 * s, 1);
     }
     mbar_init(done, 1);
     *flag = 0;
     mbar_fence_init();
   }
-  if (warp == 17) {
+  if (warp == 16) {
     tmem_alloc(smem_addr(tmem), kGTmem);
     tmem_relinquish();
   }
@@ -807,143 +844,237 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p, 
   const uint32_t tbase = *tmem;
 
   // This CTA: column group, its chunks and blocks, its k-steps.
+  // (Every groups-th block of 128 columns: the core and correction blocks at the
+  // end, which take longer to unpack, fall to different groups.)
   const int u = blockIdx.x;
-  const bool whole = u < p.full * p.s_full;
-  const int group = whole ? u / p.s_full : p.full;
-  const int split = whole ? u - group * p.s_full : u - p.full * p.s_full, splits = whole ? p.s_full : p.s_last;
-  const int c0 = group * p.nb * 4, nc = min(4 * p.nb, p.chunks - c0), nbl = (nc + 3) / 4;
+  const bool in_big = u < p.big * p.s_big;
+  const int splits = in_big ? p.s_big : p.s_small, v = in_big ? u : u - p.big * p.s_big;
+  const int group = (in_big ? 0 : p.big) + v / splits, split = v % splits;
+  const int blocks = (p.chunks + 1) / 2, nbl = (blocks - group + p.groups - 1) / p.groups;
+  const int cstep = 2 * p.groups, c0 = 2 * group;   // chunk of block b: c0 + cstep b
   const int k0 = static_cast<int>(static_cast<int64_t>(p.nk) * split / splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(p.nk) * (split + 1) / splits);
+  const int steps = k1 - k0, total = steps * nbl;
 
   if (warp < 16) {
-    const int set = warp >> 3, j = warp & 3, half = (warp >> 2) & 1, total = (k1 - k0) * nbl;
+    const int set = warp >> 2, j = warp & 3;
     const int gr = lane >> 2, cc = lane & 3;
-    // byte offsets of this lane inside a tile: row 16 j + gr, 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
-    const uint32_t row = static_cast<uint32_t>((16 * j + gr) * 128) + half * 16384u;
+    // byte offsets of this lane inside a tile: row 16 j + gr (and 64 below), 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
+    const uint32_t row = tiles + static_cast<uint32_t>((16 * j + gr) * 128);
     const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16), o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
-    RawChunk<GM> raw[kGwAhead][2];
-    int pit = set, pk = k0 + set / nbl, pb = set % nbl;   // the tile to load next
-    auto load = [&](RawChunk<GM> (&r)[2]) {
-      const int mt = 4 * pk + j, c = 4 * pb + 2 * half;
-      if (pit < total && mt < p.n_mtiles) {
-        const uint8_t* blk = p.rows.mtiles + static_cast<size_t>(mt) * p.rows.mblk_bytes;
-        if (c < nc) load_chunk<GM>(p.rows, blk, c0 + c, lane, r[0]);
-        if (c + 1 < nc) load_chunk<GM>(p.rows, blk, c0 + c + 1, lane, r[1]);
+    bool ok = true;
+    // the ring stage of this set's next tile
+    int s = set;
+    uint32_t ph = 1;
+    auto filled = [&]() {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wfull + 8 * s);
+      s += kGwSets;
+      if (s >= kGwStages) {
+        s -= kGwStages;
+        ph ^= 1u;
       }
-      pit += 2;
-      pb += 2;
+    };
+
+    // G: token 32 j + lane, columns 32 set .. + 31 of each k-step, loaded one
+    // k-step ahead and stored when this warp reaches the k-step.
+    const bool has_g = 32 * j < p.T;
+    const int nq = (p.T + 31) / 32;
+    const uint4* gsrc = p.G + (static_cast<size_t>(k0) * nq + j) * (kGwRows / 8 * 32) + 4 * set * 32 + lane;
+    const uint32_t gdst = tbase + (static_cast<uint32_t>(32 * j) << 16) + 128 * kGwBlocks + 16 * set;
+    int gi = 0;
+    uint32_t gv[16];
+    auto g_load = [&]() {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) gv[i] = 0u;
+      if (has_g && gi < steps) {
+        const uint4* src = gsrc + static_cast<size_t>(gi) * nq * (kGwRows / 8 * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 x = __ldg(src + 32 * i);
+          gv[4 * i] = x.x; gv[4 * i + 1] = x.y; gv[4 * i + 2] = x.z; gv[4 * i + 3] = x.w;
+        }
+      }
+    };
+    auto g_until = [&](int last) {   // (a warp without tokens has nothing to bring)
+      while (has_g && ok && gi <= last && gi < steps) {
+        const int q = gi & (kGwBufs - 1);
+        ok = warp_wait(flag, gempty + 8 * q, ((gi / kGwBufs) & 1) ^ 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st_32x32b_x16(gdst + (kGwRows / 2) * q, gv);
+        ++gi;
+        g_load();
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(gfull + 8 * q);
+      }
+    };
+    g_load();
+
+    // The next tile's packed bytes, both m-tiles.  Every load has its own
+    // register and at most a predicate: a load under a branch that others share a
+    // register with would have to land before the branch ends.
+    RawPair<GP> raw[2];
+    constexpr int kPer = RawPair<GP>::kPer;
+    int pk = k0, pb = set;
+    const uint8_t* pm = p.rows.mtiles + static_cast<size_t>(kGwMt * k0 + j) * p.rows.mblk_bytes;
+    const size_t next_k = static_cast<size_t>(kGwMt) * p.rows.mblk_bytes, half = static_cast<size_t>(4) * p.rows.mblk_bytes;
+    uint32_t code_off[2], scale_off[2], scale_step[2];   // of the block's chunks
+    bool core[2], corr2[2];
+    auto aim = [&]() {
       while (pb >= nbl) {
         pb -= nbl;
         ++pk;
+        pm += next_k;
+      }
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const int ks = min(c0 + cstep * pb + ch, p.chunks - 1), kc = ks - p.rows.n_res, ka = 2 * (kc - p.rows.n_L);
+        const bool res = kc < 0;
+        core[ch] = !res && ka < 0;
+        corr2[ch] = ka >= 0 && ka + 1 < p.rows.n_A;
+        code_off[ch] = lane * 16 + (res ? p.rows.off_res + ks * kResChunkBytes
+                                        : ka < 0 ? p.rows.off_Lnib + kc * kLNibChunkBytes : p.rows.off_A + ka * kAChunkBytes);
+        scale_off[ch] = gr * 4 + (res ? p.rows.off_sres + ((ks * 64) >> p.rows.g_log2) * kSresGroupBytes
+                                      : ka < 0 ? p.rows.off_sL : p.rows.off_sA);
+        scale_step[ch] = res ? kSresGroupBytes : 0;
       }
     };
+    auto load = [&](RawPair<GP>& r, int i) {
+      // (past the end of the walk or of the rows: any valid bytes)
+      const bool in = pk < k1 && kGwMt * pk + j + 4 * i < p.n_mtiles;
+      const uint8_t* m = in ? pm + (i ? half : 0) : p.rows.mtiles;
 #pragma unroll
-    for (int i = 0; i < kGwAhead; ++i) load(raw[i]);
-    int k = k0 + set / nbl, b = set % nbl;
-    bool ok = true;
-    for (int it = set; it < total && ok;) {
+      for (int ch = 0; ch < 2; ++ch) {
+        r.c[ch] = ldg128(m + code_off[ch]);
 #pragma unroll
-      for (int i = 0; i < kGwAhead; ++i) {
-        if (it >= total || !ok) break;
-        const int s = it & (kGwStages - 1), c = 4 * b + 2 * half;
-        ok = warp_wait(flag, wempty + 8 * s, ((it / kGwStages) & 1) ^ 1, p.status);
-        if (!ok) break;
-        const uint32_t tile = tiles + s * kGwTile;
-        if (4 * k + j < p.n_mtiles) {
-          if (c < nc) store_chunk<GM>(p.rows, raw[i][0], c0 + c, tile + o_lo, tile + o_hi);
-          if (c + 1 < nc) store_chunk<GM>(p.rows, raw[i][1], c0 + c + 1, tile + o_lo + 8192u, tile + o_hi + 8192u);
-        } else {
+        for (int g = 0; g < kPer; ++g) r.s[ch * kPer + g] = ldg32(m + scale_off[ch] + g * scale_step[ch]);
+        if (core[ch]) r.x[ch].x = ldg32(m + p.rows.off_Lhi + (code_off[ch] - p.rows.off_Lnib) / 4);
+        if (corr2[ch]) r.x[ch] = ldg128(m + code_off[ch] + kAChunkBytes);
+      }
+    };
+    aim();
+    load(raw[0], 0);
+    load(raw[1], 1);
+    int b = set, k = k0;
+    for (int it = set; it < total; it += kGwSets) {
+      while (b >= nbl) {
+        b -= nbl;
+        ++k;
+      }
+      g_until(k - k0);
+      if (ok) ok = warp_wait(flag, wempty + 8 * s, ph, p.status);
+      if (!ok) break;
+      const int c = c0 + cstep * b;
+      pb += kGwSets;
+      aim();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = o_lo + s * kGwTile + i * 64 * 128, hi = o_hi + s * kGwTile + i * 64 * 128;
+        if (kGwMt * k + j + 4 * i >= p.n_mtiles) {   // rows past the last m-tile
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            sts128(tile + o_lo + h * 8192u, 0u, 0u, 0u, 0u);
-            sts128(tile + o_lo + h * 8192u + 1024u, 0u, 0u, 0u, 0u);
-            sts128(tile + o_hi + h * 8192u, 0u, 0u, 0u, 0u);
-            sts128(tile + o_hi + h * 8192u + 1024u, 0u, 0u, 0u, 0u);
+            sts128(lo + h * kGwHalf, 0u, 0u, 0u, 0u);
+            sts128(lo + h * kGwHalf + 1024u, 0u, 0u, 0u, 0u);
+            sts128(hi + h * kGwHalf, 0u, 0u, 0u, 0u);
+            sts128(hi + h * kGwHalf + 1024u, 0u, 0u, 0u, 0u);
           }
+        } else if (c + 1 < p.rows.n_res) {
+          store_pair<GP>(raw[i], p.rows.sc_res, lo, hi);
+        } else {
+          store_chunk<GP>(p.rows, raw[i], c, 0, lo, hi);
+          if (c + 1 < p.chunks) store_chunk<GP>(p.rows, raw[i], c + 1, 1, lo, hi);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(wfull + 8 * s);
-        load(raw[i]);
-        it += 2;
-        b += 2;
-        while (b >= nbl) {
-          b -= nbl;
-          ++k;
-        }
+        load(raw[i], i);
       }
+      filled();
+      b += kGwSets;
     }
-    // The accumulators: lane quarter w % 4 (columns of W~), every fourth block
-    // of 128 columns, 16 tokens at a time.
-    if (warp_wait(flag, done, 0u, p.status)) {
+    g_until(steps);
+    // The accumulators: lane quarter w % 4 (tokens), every fourth piece of 32
+    // columns.  A lane's 32 columns are two runs of the dequantising lanes' 16:
+    // float4 (h, st) of them is operand columns 16 st + 4 (2 half + h) of the chunk.
+    if (warp_wait(flag, done, 0u, p.status) && has_g) {
       tc_fence_after();
-      const int q = warp & 3, m = 32 * q + lane, at = m & 63;
-      // the column's place in the operand order
-      const int pos = (m & 64) + ((at >> 2) & 3) * 16 + (at >> 4) * 4 + (at & 3);
-      float* dx = p.dx + split * p.split_stride + c0 * 64;
-      for (int blk = warp >> 2; 2 * blk < nc; blk += 4) {
-        for (int t0 = 0; t0 < p.T; t0 += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(tbase + (static_cast<uint32_t>(32 * q) << 16) + blk * p.N + t0, r);
-          tmem_ld_wait();
-          if (2 * blk + (m >> 6) < nc) {
+      const int t = 32 * j + lane;
+      float* dx = p.dx + split * p.split_stride + static_cast<size_t>(t) * p.rows.Kc;
+      for (int piece = set; piece < 4 * nbl; piece += kGwSets) {
+        const int c = c0 + cstep * (piece >> 2) + (piece >> 1 & 1);
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + (static_cast<uint32_t>(32 * j) << 16) + 32 * piece, r);
+        tmem_ld_wait();
+        if (t < p.T && c < p.chunks) {
+          float* dst = dx + c * 64 + (piece & 1) * 8;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (t0 + i < p.T) dx[static_cast<size_t>(t0 + i) * p.rows.Kc + blk * 128 + pos] = __uint_as_float(r[i]);
-          }
-          __syncwarp();
+          for (int st = 0; st < 4; ++st)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = 16 * h + 4 * st;
+              *reinterpret_cast<float4*>(dst + 16 * st + 4 * h) =
+                  make_float4(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+            }
         }
+        __syncwarp();
       }
       tc_fence_before();
     }
-  } else if (warp == 16) {
-    int issued = 0;
-    bool ok = true;
-    for (int k = k0; k < k1 && ok; ++k, ++issued) {
-      const int s = issued % p.gstages;
-      ok = warp_wait(flag, gempty + 8 * s, ((issued / p.gstages) & 1) ^ 1, p.status);
-      if (!ok) break;
-      if (elect_one()) {
-        mbar_arrive_expect_tx(gfull + 8 * s, p.g_bytes);
-        tma_load_2d(gtiles + s * p.g_bytes, &mg, k * 64, 0, gfull + 8 * s);
-      }
-      __syncwarp();
-    }
-    if (!ok) {
-      // Copies still in flight land before the block's shared memory goes away.
-      const int back = min(issued, p.gstages);
-      for (int i = 1; i <= back; ++i) mbar_wait(gfull + 8 * ((issued - i) % p.gstages), ((issued - i) / p.gstages) & 1u);
-    }
   } else {
-    const uint32_t idesc = tc_idesc_f16(128, p.N) | kTcIdescAmn;
-    const uint64_t ad0 = smem_desc_mn128(tiles, 8192u), bd0 = smem_desc_k128(gtiles);
+    // (running values and immediate offsets only, as in g_mma_warp)
+    const uint64_t bd0 = smem_desc_mn128(tiles, kGwHalf);
+    constexpr uint32_t kFull = tc_idesc_f16(128, 128) | kTcIdescBmn;
+    // of the last block, whose second chunk may not exist
+    const uint32_t last_desc = c0 + cstep * (nbl - 1) + 1 < p.chunks ? kFull : tc_idesc_f16(128, 64) | kTcIdescBmn;
+    const uint32_t a0 = tbase + 128 * kGwBlocks;
+    uint64_t bd = bd0;
+    uint32_t ad = a0, wf = wfull, we = wempty, wph = 0, gf = gfull, ge = gempty, gph = 0;
     bool ok = true;
-    int it = 0;
-    for (int k = k0; k < k1 && ok; ++k) {
-      const int gs = (k - k0) % p.gstages;
-      ok = warp_wait(flag, gfull + 8 * gs, ((k - k0) / p.gstages) & 1, p.status);
+    uint32_t acc = 0;
+    for (int k = 0; k < steps && ok; ++k) {
+      ok = warp_wait(flag, gf, gph, p.status);
       if (!ok) break;
-      const uint64_t bd = bd0 + static_cast<uint64_t>(gs) * (p.g_bytes >> 4);
-      for (int b = 0; b < nbl; ++b, ++it) {
-        const int s = it & (kGwStages - 1);
-        ok = warp_wait(flag, wfull + 8 * s, (it / kGwStages) & 1, p.status);
+      uint32_t d = tbase;
+      for (int b = 0; b < nbl; ++b) {
+        ok = warp_wait(flag, wf, wph, p.status);
         if (!ok) break;
         tc_fence_after();
+        const bool last = b == nbl - 1;
+        const uint32_t idesc = last ? last_desc : kFull;
         if (elect_one()) {
-          const uint64_t a = ad0 + static_cast<uint64_t>(s) * (kGwTile >> 4);
-          const uint32_t d = tbase + 2 * b * p.N;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (4 * b + 2 * i < nc) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                tc_mma_ss(d + i * p.N, a + i * 1024 + e * 128, bd + 2 * e, idesc, (k != k0 || e != 0) ? 1u : 0u);
-            }
-          }
-          tc_commit(wempty + 8 * s);
-          if (b == nbl - 1) tc_commit(gempty + 8 * gs);
+          tc_mma_ts(d, ad, bd, idesc, acc);
+          tc_mma_ts(d, ad + 8, bd + 128, idesc, 1u);
+          tc_mma_ts(d, ad + 16, bd + 256, idesc, 1u);
+          tc_mma_ts(d, ad + 24, bd + 384, idesc, 1u);
+          tc_mma_ts(d, ad + 32, bd + 512, idesc, 1u);
+          tc_mma_ts(d, ad + 40, bd + 640, idesc, 1u);
+          tc_mma_ts(d, ad + 48, bd + 768, idesc, 1u);
+          tc_mma_ts(d, ad + 56, bd + 896, idesc, 1u);
+          tc_commit(we);
+          if (last) tc_commit(ge);
         }
         __syncwarp();
+        d += 128;
+        bd += kGwTile >> 4;
+        wf += 8;
+        we += 8;
+        if (wf == wempty) {   // the ring wraps
+          bd = bd0;
+          wf = wfull;
+          we = wempty;
+          wph ^= 1u;
+        }
+      }
+      acc = 1;
+      ad += kGwRows / 2;
+      gf += 8;
+      ge += 8;
+      if (gf == gempty) {
+        ad = a0;
+        gf = gfull;
+        ge = gempty;
+        gph ^= 1u;
       }
     }
     if (ok && elect_one()) tc_commit(done);
@@ -951,7 +1082,7 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p, 
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tbase, kGTmem);
   }
@@ -962,24 +1093,25 @@ constexpr int kFewTokens = 128;   // up to here the packed rows are dequantised 
 
 // Work split of gw_kernel.
 struct GwPlan {
-  int N, nb, chunks, full, s_full, s_last, nk;
+  int chunks, groups, big, s_big, s_small, nk;
 };
-GwPlan gw_plan(const archead_handle& h, int T) {
+GwPlan gw_plan(const archead_handle& h) {
   GwPlan g{};
-  g.N = (T + 15) / 16 * 16;
   g.chunks = tc_kc(h.L) / 64;
-  g.nk = (h.L.n_mtiles + 3) / 4;
-  // As many column blocks as the TMEM holds (G is read once per group), fewer
-  // where the head is too small to give every SM a few tiles.
-  for (g.nb = kGwMaxN / g.N; g.nb > 1; --g.nb)
-    if (static_cast<int64_t>((g.chunks + 4 * g.nb - 1) / (4 * g.nb)) * g.nk >= 8 * h.num_sms) break;
-  g.full = g.chunks / (4 * g.nb);
-  const int rest = g.chunks - g.full * 4 * g.nb;
-  const auto share = [&](int c) {
-    return std::max(1, std::min(g.nk, static_cast<int>(static_cast<int64_t>(h.num_sms) * c / g.chunks)));
+  g.nk = (h.L.n_mtiles + kGwMt - 1) / kGwMt;
+  const int blocks = (g.chunks + 1) / 2;
+  // Three blocks per CTA read G least; fewer where the head is too small to
+  // give every SM a few tiles.  Groups of nb and nb - 1 blocks, with row splits
+  // in proportion: every CTA has about the same number of tiles.
+  int nb = std::min(kGwBlocks, blocks);
+  while (nb > 1 && static_cast<int64_t>((blocks + nb - 1) / nb) * g.nk < 4 * h.num_sms) --nb;
+  g.groups = (blocks + nb - 1) / nb;
+  g.big = g.groups - (g.groups * nb - blocks);
+  const auto share = [&](int b) {
+    return std::max(1, std::min(g.nk, static_cast<int>(static_cast<int64_t>(h.num_sms) * b / blocks)));
   };
-  g.s_full = g.full > 0 ? share(4 * g.nb) : 0;
-  g.s_last = rest > 0 ? share(rest) : 0;
+  g.s_big = share(nb);
+  g.s_small = share(std::max(1, nb - 1));
   return g;
 }
 
@@ -1008,11 +1140,10 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     // The forward call's workspace comes first: its header is this one's.
     o.fwd = ws_layout(h, T).total;
     at = round_up(o.fwd, 256);
-    o.pitch = static_cast<int>(round_up(L.Vp, 64));
-    o.n_ssum = (L.Vp + kGPiece - 1) / kGPiece;
+    o.n_ssum = (L.n_mtiles + kGwMt - 1) / kGwMt;
     o.logits = take(t * L.V * 4);
-    const GwPlan g = gw_plan(h, T);
-    o.splits = std::max(g.s_full, g.s_last);
+    const GwPlan g = gw_plan(h);
+    o.splits = std::max(g.s_big, g.s_small);
   } else {
     const int n_chunks = (L.Vp + kGradChunk - 1) / kGradChunk;
     o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
@@ -1027,7 +1158,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
   }
   o.ssum = take(o.n_ssum * t * 4);
-  o.g = take(t * o.pitch * 2);
+  o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
   o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
@@ -1134,12 +1265,12 @@ int grad_lowrank(const GradCall& c) {
 }
 
 // dX -> dh of one pass's tokens.
-int grad_finish(const GradCall& c, GemmParams& p, int splits, int splits_last, int last) {
+int grad_finish(const GradCall& c, GemmParams& p, int splits, int splits_small, int groups, int big) {
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
   DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, c.o.n_ssum, nt, Kc, L.d,
-              L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, splits_last, last};
+              L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, splits_small, groups, big};
   dx_kernel<<<dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream>>>(dp);
   cudaError_t e = cudaGetLastError();
   CUtensorMap mz{}, mr{};
@@ -1165,39 +1296,33 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
   const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
   if (rc != ARCHEAD_OK) return rc;
-  GParams gp{logits, p.lse, p.grad, p.targets, p.G, p.ssum, T, L.V, L.Vp, h.row0, c.o.pitch};
-  g_kernel<<<dim3(c.o.n_ssum, T), 256, 0, c.stream>>>(gp);
+  GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0};
+  g_kernel<<<dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream>>>(gp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e);
-  const GwPlan g = gw_plan(h, T);
+  const GwPlan g = gw_plan(h);
   GwParams w{};
   w.rows = dequant_params(h, nullptr);
+  w.G = gp.G;
+  w.T = T;
   w.n_mtiles = L.n_mtiles;
   w.nk = g.nk;
-  w.T = T;
-  w.N = g.N;
-  w.nb = g.nb;
   w.chunks = g.chunks;
-  w.full = g.full;
-  w.s_full = g.s_full;
-  w.s_last = g.s_last;
-  w.g_bytes = static_cast<uint32_t>(g.N) * 128u;
-  w.gstages = static_cast<int>(std::min<uint32_t>(4, (kGwSmemMax - kGwGOff - 256) / w.g_bytes));
-  w.bar_off = kGwGOff + w.gstages * w.g_bytes;
+  w.groups = g.groups;
+  w.big = g.big;
+  w.s_big = g.s_big;
+  w.s_small = g.s_small;
   w.dx = p.dx;
   w.split_stride = p.split_stride;
   w.status = p.status;
-  CUtensorMap mg;
-  e = tc_encode_map(&mg, p.G, L.Vp, T, c.o.pitch, g.N);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  const int grid = g.full * g.s_full + g.s_last;
-  const uint32_t smem = w.bar_off + 256 + 1024;
-  if (w.rows.g_log2 >= 6) gw_kernel<0><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
-  else if (w.rows.g_log2 == 5) gw_kernel<1><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
-  else gw_kernel<2><<<grid, kGwWarps * 32, smem, c.stream>>>(w, mg);
+  const int grid = g.big * g.s_big + (g.groups - g.big) * g.s_small;
+  if (w.rows.g_log2 >= 7) gw_kernel<1><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
+  else if (w.rows.g_log2 == 6) gw_kernel<2><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
+  else if (w.rows.g_log2 == 5) gw_kernel<4><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
+  else gw_kernel<8><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
   e = cudaGetLastError();
   if (e != cudaSuccess) return set_cuda_error(e);
-  return grad_finish(c, p, g.s_full, g.s_last, g.full * g.nb * 256);
+  return grad_finish(c, p, g.s_big, g.s_small, g.groups, g.big);
 }
 
 // Many tokens: chunk by chunk through the dequantised rows.
@@ -1238,7 +1363,7 @@ int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
     e = launch_gemm<kAccumulate>(p, mg, mwn, h.num_sms, c.stream);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
-  return grad_finish(c, p, o.splits, o.splits, Kc);
+  return grad_finish(c, p, o.splits, o.splits, 1, 1);
 }
 
 int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T, const int32_t* targets,
@@ -1287,9 +1412,9 @@ cudaError_t grad_set_attributes() {
     e = cudaFuncSetAttribute(grad_gemm_kernel<kAccumulate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(grad_gemm_kernel<kFinish>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
-  for (const void* k : {reinterpret_cast<const void*>(&gw_kernel<0>), reinterpret_cast<const void*>(&gw_kernel<1>),
-                        reinterpret_cast<const void*>(&gw_kernel<2>)})
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGwSmemMax + 1024);
+  for (const void* k : {reinterpret_cast<const void*>(&gw_kernel<1>), reinterpret_cast<const void*>(&gw_kernel<2>),
+                        reinterpret_cast<const void*>(&gw_kernel<4>), reinterpret_cast<const void*>(&gw_kernel<8>)})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGwSmem);
   return e;
 }
 
