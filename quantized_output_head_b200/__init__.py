@@ -358,14 +358,13 @@ class PackedHead:
         if targets.shape != (T,):
             raise ValueError("targets must hold one id per token")
         lse, grad_ce = _check_tokens("lse", lse, T, self.device), _check_tokens("grad_ce", grad_ce, T, self.device)
-        with torch.cuda.device(self.device):
-            out = torch.empty((T, self.d), dtype=out_dtype, device=self.device)
-            if workspace is None:
-                workspace = torch.empty(self.grad_workspace_bytes(T), dtype=torch.uint8, device=self.device)
+        out = hidden.new_empty((T, self.d), dtype=out_dtype)
+        if workspace is None:
+            workspace = hidden.new_empty(self.grad_workspace_bytes(T), dtype=torch.uint8)
+        with _on_device(self.device) as stream:
             _check(_lib.archead_grad_hidden(self.handle, hidden.data_ptr(), T, targets.data_ptr(), lse.data_ptr(),
                                             grad_ce.data_ptr(), out.data_ptr(), GRAD_DTYPES[out_dtype],
-                                            workspace.data_ptr(), workspace.numel(), _stream_ptr(None)),
-                   "archead_grad_hidden")
+                                            workspace.data_ptr(), workspace.numel(), stream), "archead_grad_hidden")
         return out
 
     # --------------------------------------------------- vocabulary shards
@@ -532,12 +531,12 @@ def policy_loss(ce: torch.Tensor, ce_old: torch.Tensor, advantages: torch.Tensor
     if mask is not None:
         mask = _check_mask(mask, T, device)
     opts = ArcheadPolicyOptions(clip_low, clip_high, kl_coef, scale, REDUCTIONS[reduction], ADVANTAGES[advantage_per])
-    with torch.cuda.device(device):
-        grad, few, ws = _loss_buffers(T, 4, S, device)
-        at = few.data_ptr()
+    few, grad, ws = ce.new_empty(4), torch.empty_like(ce), ce.new_empty(_loss_workspace(S))
+    at = few.data_ptr()
+    with _on_device(device) as stream:
         _check(_lib.archead_policy_loss(ce.data_ptr(), ce_old.data_ptr(), advantages.data_ptr(), _ptr(ce_ref), _ptr(mask),
                                         _ptr(cu_seqlens), T, S, ctypes.byref(opts), at, grad.data_ptr(), at + 4,
-                                        ws.data_ptr(), ws.numel(), _stream_ptr(None)), "archead_policy_loss")
+                                        ws.data_ptr(), 4 * ws.shape[0], stream), "archead_policy_loss")
     return few[0], grad, few[1:]
 
 
@@ -566,19 +565,47 @@ def preference_loss(ce: torch.Tensor, cu_seqlens: torch.Tensor, *, mask: Optiona
     if mask is not None:
         mask = _check_mask(mask, T, device)
     opts = ArcheadPreferenceOptions(beta, margin, label_smoothing, scale, PREFERENCES[kind], 1 if average else 0)
-    with torch.cuda.device(device):
-        grad, few, ws = _loss_buffers(T, 1 + S, S, device)
-        at = few.data_ptr()
+    few, grad, ws = ce.new_empty(1 + S), torch.empty_like(ce), ce.new_empty(_loss_workspace(S))
+    at = few.data_ptr()
+    with _on_device(device) as stream:
         _check(_lib.archead_preference_loss(ce.data_ptr(), _ptr(ce_ref), _ptr(mask), cu_seqlens.data_ptr(), T, S // 2,
-                                            ctypes.byref(opts), at, grad.data_ptr(), at + 4, ws.data_ptr(), ws.numel(),
-                                            _stream_ptr(None)), "archead_preference_loss")
+                                            ctypes.byref(opts), at, grad.data_ptr(), at + 4, ws.data_ptr(), 4 * ws.shape[0],
+                                            stream), "archead_preference_loss")
     return few[0], grad, few[1:].view(2, S // 2)
 
 
-def _loss_buffers(T, n_few, S, device):
-    """The gradient, the small outputs (one tensor) and the workspace of a loss call."""
-    return (torch.empty(T, dtype=torch.float32, device=device), torch.empty(n_few, dtype=torch.float32, device=device),
-            torch.empty(_lib.archead_loss_workspace_bytes(S), dtype=torch.uint8, device=device))
+def _loss_workspace(S) -> int:
+    """Workspace of a loss call, in floats (allocated for the call: its order on
+    the stream, and a graph's own pool, are the allocator's business)."""
+    return _lib.archead_loss_workspace_bytes(S) // 4
+
+
+class _on_device:
+    """`with _on_device(d) as stream`: d is the current device inside, stream its
+    current stream's handle.  (torch.cuda.device and current_stream cost more
+    than the launch; the common case, d already current, needs neither.)"""
+    __slots__ = ("device", "guard")
+
+    def __init__(self, device):
+        self.device, self.guard = device, None
+
+    def __enter__(self) -> int:
+        if torch.cuda.current_device() != self.device.index:
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return _raw_stream(self.device.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _raw_stream(index: int) -> int:
+    return int(torch.cuda.current_stream(index).cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _token_count(name, x) -> int:

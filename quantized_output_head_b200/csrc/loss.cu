@@ -15,14 +15,16 @@
 //   squared  l = (D - 1 / (2 beta))^2
 // averaged over the pairs; every counted token of a sequence gets the slope.
 //
-// One launch of one cluster of up to 16 blocks does the whole call: the phases
-// (counts and sums per sequence; per-pair or per-sequence factors; gradients)
-// meet at hardware cluster barriers, so there is no counter to clear and no
-// second launch.  Each warp owns a contiguous run of tokens, cut at sequence
-// boundaries; the piece of a sequence in a later warp's run goes to that
-// warp's slot and the pieces are added in run order, so results do not depend
-// on timing.  What bounds it: launch and barrier latency up to ~10^5 tokens,
-// the cluster's share of L2 bandwidth at 10^6.
+// One launch does the whole call: the phases (counts and sums per sequence;
+// per-pair or per-sequence factors; gradients; the loss) meet at a barrier of
+// all its blocks, so there is no counter to clear and no second launch: one
+// block up to kOneBlock tokens, one cluster of up to 16 with the cluster's
+// hardware barrier up to kOneCluster, above that a cooperative grid of up to
+// one block per SM.  Each warp owns a contiguous run of tokens, cut at sequence
+// boundaries; the piece of a sequence in a later warp's run goes to that warp's
+// slot and the pieces are added in run order, so results do not depend on
+// timing.  What bounds it: launch, barrier and load latency; at 10^6 tokens the
+// fp64 arithmetic is about a third.
 //
 // All sums, log-ratios and exponentials are fp64: a log-ratio decides on which
 // side of a clipping border a token lies, exp(d) - 1 - d is of second order in
@@ -30,7 +32,9 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include "device.cuh"
 #include "handle.h"
@@ -41,9 +45,11 @@ namespace archead {
 
 namespace {
 
-constexpr int kLossThreads = 1024, kLossWarps = kLossThreads / 32, kLossMaxCluster = 16;
-constexpr int kMaxUnits = kLossWarps * kLossMaxCluster;
-constexpr int kGroup = 128;   // tokens of a warp iteration: four consecutive ones per lane
+constexpr int kLossThreads = 1024, kLossWarps = kLossThreads / 32;
+constexpr int kLossMaxBlocks = 160;   // of the cooperative grid (one per SM, 148 here)
+constexpr int kMaxUnits = kLossWarps * kLossMaxBlocks;
+constexpr int kGroup = 128;           // tokens of a warp iteration: four consecutive ones per lane
+constexpr int kOneBlock = kLossWarps * kGroup, kOneCluster = 16 * kOneBlock;
 
 struct TokenArgs {
   const float* ce;
@@ -58,6 +64,8 @@ struct TokenArgs {
   int32_t* seg_n;             // the same for counted tokens
   int32_t* open_n;
   float* coef;                // [S] per-sequence factor
+  double* part;               // [blocks][4] sums of a block
+  int32_t* part_n;            // [blocks][2]
 };
 
 struct PolicyArgs {
@@ -83,17 +91,35 @@ __device__ __forceinline__ int cu_at(const TokenArgs& a, int s) {
   return min(max(__ldg(a.cu + s), 0), a.T);
 }
 
-// The last s with cu[s] <= t, from lo on; -1 if there is none.
-__device__ __forceinline__ int seq_of(const TokenArgs& a, int t, int lo) {
-  int hi = a.S;   // cu[S] ends the last sequence
-  lo = max(lo, 0);
-  if (cu_at(a, lo) > t) return -1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_at(a, mid) <= t) lo = mid;
-    else hi = mid - 1;
+// The last s in [0, S] with cu[s] <= t, -1 if there is none (cu[S] ends the last
+// sequence); the same t in every lane, 32 probes a round.
+__device__ __forceinline__ int seq_of_warp(const TokenArgs& a, int t, int lane) {
+  int lo = 0, hi = a.S;
+  for (;;) {
+    const int step = (hi - lo + 32) / 32, at = lo + lane * step;
+    const int n = __popc(__ballot_sync(0xffffffffu, at <= hi && cu_at(a, min(at, a.S)) <= t));
+    if (n == 0) return lo - 1;
+    lo += (n - 1) * step;
+    if (step == 1) return lo;
+    hi = min(hi, lo + step - 1);
   }
-  return lo;
+}
+
+// The same per lane, from `from` on (whose offset is <= t): doubling steps, then
+// halving ones.
+__device__ __forceinline__ int seq_from(const TokenArgs& a, int t, int from) {
+  if (from < 0) {
+    if (cu_at(a, 0) > t) return -1;
+    from = 0;
+  }
+  int step = 1;
+  while (from + step <= a.S && cu_at(a, from + step) <= t) {
+    from += step;
+    step *= 2;
+  }
+  for (step /= 2; step > 0; step /= 2)
+    if (from + step <= a.S && cu_at(a, from + step) <= t) from += step;
+  return from;
 }
 
 __device__ __forceinline__ void load4(const float* p, int t, int T, bool vec, float (&v)[4]) {
@@ -173,7 +199,7 @@ template <bool kSum>
 __device__ void walk_segments(const TokenArgs& a, int unit, int lane) {
   const int u0 = unit * a.unit, u1 = min(u0 + a.unit, a.T);
   if (u0 >= u1) return;
-  int s = seq_of(a, u0, 0);
+  int s = seq_of_warp(a, u0, lane);
   if (s < 0) s = 0;   // the run begins before the first sequence
   double sum = 0.0;
   int n = 0;
@@ -247,7 +273,7 @@ template <class F>
 __device__ __forceinline__ void for_tokens(const TokenArgs& a, int unit, int lane, F body) {
   const int u0 = unit * a.unit, u1 = min(u0 + a.unit, a.T);
   if (u0 >= u1) return;
-  int s = seq_of(a, u0, 0);
+  int s = seq_of_warp(a, u0, lane);
   for (int g = u0; g < u1; g += kGroup) {
     const int t = g + 4 * lane;
     int q[4];
@@ -259,7 +285,7 @@ __device__ __forceinline__ void for_tokens(const TokenArgs& a, int unit, int lan
       int from = s;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int z = seq_of(a, min(t + i, a.T - 1), from);
+        int z = seq_from(a, min(t + i, a.T - 1), from);
         from = z;
         if (z >= a.S || (z >= 0 && t + i >= cu_at(a, z + 1))) z = -1;
         q[i] = z;
@@ -270,27 +296,52 @@ __device__ __forceinline__ void for_tokens(const TokenArgs& a, int unit, int lan
   }
 }
 
-__device__ __forceinline__ void cluster_meet() { cg::this_cluster().sync(); }
+// Barrier of all blocks of the launch, with their writes before it visible after
+// it: of one block, of one cluster, of a cooperative grid.
+enum MeetKind { kMeetBlock, kMeetCluster, kMeetGrid };
+template <MeetKind kMeet>
+__device__ __forceinline__ void meet() {
+  if constexpr (kMeet == kMeetBlock) __syncthreads();
+  else if constexpr (kMeet == kMeetCluster) cg::this_cluster().sync();
+  else cg::this_grid().sync();
+}
+
+// Sums over the warps of this block, in warp order, of N values that lane 0 of
+// each holds -> part[block].
+template <int N>
+__device__ __forceinline__ void block_sums(const TokenArgs& a, const double (&v)[N], int warp, int lane) {
+  __shared__ double sums[kLossWarps][N];
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) sums[warp][i] = v[i];
+  __syncthreads();
+  if (threadIdx.x < N) {
+    double x = 0.0;
+    for (int w = 0; w < kLossWarps; ++w) x += sums[w][threadIdx.x];
+    a.part[4 * blockIdx.x + threadIdx.x] = x;
+  }
+}
+// The sum of value i over all blocks, by one warp (the same order every time).
+__device__ __forceinline__ double all_blocks(const TokenArgs& a, int i, int lane) {
+  double x = 0.0;
+  for (int b = lane; b < gridDim.x; b += 32) x += __ldcg(a.part + 4 * b + i);
+  return warp_sum(x);
+}
 
 }  // namespace
 
+template <MeetKind kMeet>
 __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const PolicyArgs p) {
-  __shared__ double part[kLossWarps][4];
-  __shared__ int count[2];        // counted tokens, sequences with any (this block's share)
+  __shared__ int count[2], counts[2];   // counted tokens, sequences with any: this block's share, of all
   const TokenArgs& a = p.a;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = cl.block_rank(), blocks = cl.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = rank * kLossWarps + warp, units = blocks * kLossWarps;
+  const int unit = blockIdx.x * kLossWarps + warp, units = gridDim.x * kLossWarps;
   if (threadIdx.x < 2) count[threadIdx.x] = 0;
   __syncthreads();
-  // Counted tokens per sequence (integers: the order of the adds is free).
   const bool by_sequence = p.reduction == ARCHEAD_REDUCE_SEQUENCES;
-  if (a.mask != nullptr) {
-    if (by_sequence) {
-      walk_segments<false>(a, unit, lane);
-      cluster_meet();
-    }
+  if (a.mask != nullptr && by_sequence) {
+    walk_segments<false>(a, unit, lane);
+    meet<kMeet>();
   }
   int total = 0, alive = 0;
   if (by_sequence) {
@@ -312,19 +363,23 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
   } else if (unit == 0) {
     total = max(0, cu_at(a, a.S) - cu_at(a, 0));
   }
-  if (lane == 0 && (total != 0 || alive != 0)) {
+  if (lane == 0 && (total != 0 || alive != 0)) {   // (integers: the order of the adds is free)
     atomicAdd(&count[0], total);
     atomicAdd(&count[1], alive);
   }
-  cluster_meet();
-  total = alive = 0;
-  for (int b = 0; b < blocks; ++b) {
-    const int* c = cl.map_shared_rank(count, b);
-    total += c[0];
-    alive += c[1];
+  __syncthreads();
+  if (threadIdx.x < 2) a.part_n[2 * blockIdx.x + threadIdx.x] = count[threadIdx.x];
+  meet<kMeet>();
+  if (warp < 2) {
+    int n = 0;
+    for (int b = lane; b < gridDim.x; b += 32) n += __ldcg(a.part_n + 2 * b + warp);
+    n = warp_sum(n);
+    if (lane == 0) counts[warp] = n;
   }
+  __syncthreads();
+  total = counts[0];
   const double all = p.reduction == ARCHEAD_REDUCE_SUM ? p.scale
-                     : by_sequence                     ? p.scale / max(alive, 1)
+                     : by_sequence                     ? p.scale / max(counts[1], 1)
                                                        : p.scale / max(total, 1);
   double loss = 0.0, cut_n = 0.0, kl_old = 0.0, kl_ref = 0.0;
   for_tokens(a, unit, lane, [&](int t, const int (&q)[4]) {
@@ -363,38 +418,24 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
     }
     store4(a.grad, t, a.T, a.vec, g);
   });
-  loss = warp_sum(loss);
-  cut_n = warp_sum(cut_n);
-  kl_old = warp_sum(kl_old);
-  kl_ref = warp_sum(kl_ref);
-  if (lane == 0) {
-    part[warp][0] = loss;
-    part[warp][1] = cut_n;
-    part[warp][2] = kl_old;
-    part[warp][3] = kl_ref;
-  }
-  cluster_meet();
-  if (rank == 0 && threadIdx.x < 4) {
-    double v = 0.0;
-    for (int b = 0; b < blocks; ++b) {
-      const double* c = cl.map_shared_rank(&part[0][0], b);
-      for (int w = 0; w < kLossWarps; ++w) v += c[4 * w + threadIdx.x];
+  block_sums<4>(a, {warp_sum(loss), warp_sum(cut_n), warp_sum(kl_old), warp_sum(kl_ref)}, warp, lane);
+  meet<kMeet>();
+  if (blockIdx.x == 0 && warp < 4) {
+    const double v = all_blocks(a, warp, lane);
+    if (lane == 0) {
+      if (warp == 0) *p.loss = static_cast<float>(v);
+      else p.stats[warp - 1] = static_cast<float>(v / max(total, 1));
     }
-    if (threadIdx.x == 0) *p.loss = static_cast<float>(v);
-    else p.stats[threadIdx.x - 1] = static_cast<float>(v / max(total, 1));
   }
-  cluster_meet();   // the others' shared memory stays until it has been read
 }
 
+template <MeetKind kMeet>
 __global__ void __launch_bounds__(kLossThreads, 1) preference_loss_kernel(const PreferenceArgs p) {
-  __shared__ double part[kLossWarps];
   const TokenArgs& a = p.a;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = cl.block_rank(), blocks = cl.num_blocks();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = rank * kLossWarps + warp, units = blocks * kLossWarps;
+  const int unit = blockIdx.x * kLossWarps + warp, units = gridDim.x * kLossWarps;
   walk_segments<true>(a, unit, lane);
-  cluster_meet();
+  meet<kMeet>();
   double loss = 0.0;
   for (int i = unit; i < p.N; i += units) {
     double sc, sr;
@@ -429,8 +470,8 @@ __global__ void __launch_bounds__(kLossThreads, 1) preference_loss_kernel(const 
       p.rewards[p.N + i] = static_cast<float>(p.beta * sr);
     }
   }
-  if (lane == 0) part[warp] = loss;
-  cluster_meet();
+  block_sums<1>(a, {loss}, warp, lane);
+  meet<kMeet>();
   for_tokens(a, unit, lane, [&](int t, const int (&q)[4]) {
     if (t >= a.T) return;
     const uint32_t keep = keep4(a, t);
@@ -439,15 +480,10 @@ __global__ void __launch_bounds__(kLossThreads, 1) preference_loss_kernel(const 
     for (int i = 0; i < 4; ++i) g[i] = q[i] >= 0 && (keep >> i & 1u) ? a.coef[q[i]] : 0.f;
     store4(a.grad, t, a.T, a.vec, g);
   });
-  if (rank == 0 && threadIdx.x == 0) {
-    double v = 0.0;
-    for (int b = 0; b < blocks; ++b) {
-      const double* c = cl.map_shared_rank(&part[0], b);
-      for (int w = 0; w < kLossWarps; ++w) v += c[w];
-    }
-    *p.loss = static_cast<float>(p.N > 0 ? v * p.scale / p.N : 0.0);
+  if (blockIdx.x == 0 && warp == 0) {
+    const double v = all_blocks(a, 0, lane);
+    if (lane == 0) *p.loss = static_cast<float>(p.N > 0 ? v * p.scale / p.N : 0.0);
   }
-  cluster_meet();
 }
 
 namespace {
@@ -458,7 +494,7 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 
 // Workspace: pieces per sequence and per unit, factors per sequence.
 struct LossLayout {
-  size_t seg_sum, open_sum, seg_n, open_n, coef, total;
+  size_t seg_sum, open_sum, seg_n, open_n, coef, part, part_n, total;
 };
 LossLayout loss_layout(int S) {
   LossLayout o{};
@@ -474,14 +510,27 @@ LossLayout loss_layout(int S) {
   o.seg_n = take(s * 4);
   o.open_n = take(kMaxUnits * 4);
   o.coef = take(s * 4);
+  o.part = take(kLossMaxBlocks * 32);
+  o.part_n = take(kLossMaxBlocks * 8);
   o.total = at;
   return o;
 }
 
-// Blocks of the cluster: enough that a warp's run is one or two groups.
-int loss_blocks(int T) {
+// Blocks of a call: a warp's run is one group of tokens while that many blocks
+// fit.  Also sets up the device on its first call (clusters of more than 8
+// blocks are opted into).
+struct LossDevice {
+  std::once_flag once;
+  int sms = 0;
+  cudaError_t error = cudaSuccess;
+};
+constexpr int kMaxDevices = 64;
+LossDevice g_loss_device[kMaxDevices];
+
+int loss_blocks(int T, int sms) {
+  if (T > kOneCluster) return std::min(sms, kLossMaxBlocks);
   int b = 1;
-  while (b < kLossMaxCluster && T > b * kLossWarps * kGroup) b *= 2;
+  while (T > b * kOneBlock) b *= 2;
   return b;
 }
 
@@ -504,25 +553,60 @@ void token_args(TokenArgs& a, const float* ce, const float* ce_ref, const uint8_
   a.seg_n = reinterpret_cast<int32_t*>(w + o.seg_n);
   a.open_n = reinterpret_cast<int32_t*>(w + o.open_n);
   a.coef = reinterpret_cast<float*>(w + o.coef);
+  a.part = reinterpret_cast<double*>(w + o.part);
+  a.part_n = reinterpret_cast<int32_t*>(w + o.part_n);
 }
 
 template <class Args>
-int launch_loss(void (*kernel)(Args), const Args& args, int blocks, archead_stream_t stream) {
-  cudaError_t e = cudaSuccess;
-  if (blocks > 8)   // clusters of more than 8 blocks are opted into per device
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+struct LossKernels {
+  void (*block)(Args);
+  void (*cluster)(Args);
+  void (*grid)(Args);
+};
+constexpr LossKernels<PolicyArgs> kPolicy{policy_loss_kernel<kMeetBlock>, policy_loss_kernel<kMeetCluster>,
+                                          policy_loss_kernel<kMeetGrid>};
+constexpr LossKernels<PreferenceArgs> kPreference{preference_loss_kernel<kMeetBlock>, preference_loss_kernel<kMeetCluster>,
+                                                  preference_loss_kernel<kMeetGrid>};
+
+int loss_device(int* sms) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return set_cuda_error(e);
+  if (dev < 0 || dev >= kMaxDevices) return ARCHEAD_EUNSUP;
+  LossDevice& d = g_loss_device[dev];
+  std::call_once(d.once, [&]() {
+    d.error = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (d.error == cudaSuccess)
+      d.error = cudaFuncSetAttribute(kPolicy.cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (d.error == cudaSuccess)
+      d.error = cudaFuncSetAttribute(kPreference.cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (d.error != cudaSuccess) return set_cuda_error(d.error);
+  *sms = d.sms;
+  return ARCHEAD_OK;
+}
+
+template <class Args>
+int launch_loss(const LossKernels<Args>& kernels, const Args& args, int blocks, archead_stream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kLossThreads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = blocks;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  void (*kernel)(Args) = kernels.block;
+  if (blocks > 16) {
+    kernel = kernels.grid;
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else if (blocks > 1) {
+    kernel = kernels.cluster;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, args);
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
   return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
 }
 
@@ -559,7 +643,10 @@ extern "C" ARCHEAD_API int archead_policy_loss(const float* ce, const float* ce_
     if (!aligned(q, 4)) return ARCHEAD_EALIGN;
   if (!aligned(workspace, 256)) return ARCHEAD_EALIGN;
   if (workspace_bytes < loss_layout(n_sequences).total) return ARCHEAD_ENOMEM;
-  const int blocks = loss_blocks(T);
+  int sms = 0;
+  const int rc = loss_device(&sms);
+  if (rc != ARCHEAD_OK) return rc;
+  const int blocks = loss_blocks(T, sms);
   PolicyArgs p{};
   token_args(p.a, ce, ce_ref, mask, cu_seqlens, T, n_sequences, grad_ce, workspace, blocks);
   if (!aligned(ce_old, 16) || (!per_sequence && !aligned(advantages, 16))) p.a.vec = 0;
@@ -575,7 +662,7 @@ extern "C" ARCHEAD_API int archead_policy_loss(const float* ce, const float* ce_
   p.per_sequence = per_sequence ? 1 : 0;
   p.loss = loss;
   p.stats = stats;
-  return launch_loss(policy_loss_kernel, p, blocks, stream);
+  return launch_loss(kPolicy, p, blocks, stream);
 }
 
 extern "C" ARCHEAD_API int archead_preference_loss(const float* ce, const float* ce_ref, const uint8_t* mask,
@@ -599,7 +686,10 @@ extern "C" ARCHEAD_API int archead_preference_loss(const float* ce, const float*
     if (!aligned(q, 4)) return ARCHEAD_EALIGN;
   if (!aligned(workspace, 256)) return ARCHEAD_EALIGN;
   if (workspace_bytes < loss_layout(2 * n_pairs).total) return ARCHEAD_ENOMEM;
-  const int blocks = loss_blocks(T);
+  int sms = 0;
+  const int rc = loss_device(&sms);
+  if (rc != ARCHEAD_OK) return rc;
+  const int blocks = loss_blocks(T, sms);
   PreferenceArgs p{};
   token_args(p.a, ce, ce_ref, mask, cu_seqlens, T, 2 * n_pairs, grad_ce, workspace, blocks);
   p.beta = o.beta;
@@ -611,5 +701,5 @@ extern "C" ARCHEAD_API int archead_preference_loss(const float* ce, const float*
   p.average = o.average != 0;
   p.loss = loss;
   p.rewards = rewards;
-  return launch_loss(preference_loss_kernel, p, blocks, stream);
+  return launch_loss(kPreference, p, blocks, stream);
 }

@@ -205,10 +205,11 @@ def test_offsets_outside_the_tokens_touch_nothing_else(qoh):
         assert rc == 0 and torch.all(buf[:32] == 7) and torch.all(buf[32 + T:] == 7) and torch.all(ws[n:] == 255)
 
 
-def test_losses_on_another_stream_and_in_a_graph(qoh):
+@pytest.mark.parametrize("lengths", [[90, 3, 0, 1000], [900, 3000, 0, 10000], [30000, 70000, 1, 55000]])
+def test_losses_on_another_stream_and_in_a_graph(qoh, lengths):
     """Two captured graphs and eager calls side by side give the same bits, and a
-    replay reads the inputs as they are then."""
-    rng, cu, T, ce, old, ref, mask = tokens([900, 3000, 0, 10000], 21)
+    replay reads the inputs as they are then (one block, a cluster, a grid)."""
+    rng, cu, T, ce, old, ref, mask = tokens(lengths, 21)
     ce_d, old_d, ref_d, mask_d, cu_d = (dev(x) for x in (ce, old, ref, mask, cu))
     adv = dev(rng.standard_normal(4).astype(np.float32))
 
