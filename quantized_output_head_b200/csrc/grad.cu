@@ -291,13 +291,17 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
 }
 
 // -------------------------------------------------------------------- gemm
-// D[128 tokens x 256 columns] tiles of A B, A [tokens][K] fp16 K-major, B fp16
+// D[256 tokens x 256 columns] tiles of A B, A [tokens][K] fp16 K-major, B fp16
 // either [columns][K] (softmax) or [K][columns] (accumulate, finish), by TMA in
-// k-steps of 64.  One CTA per SM walks its units (K split, token tile, column
-// tile); warp 0 issues the copies, warp 1 the MMAs, warps 2-5 empty one of two
-// TMEM accumulators while the next fills.
-constexpr int kGM = 128, kGN = 256, kGStages = 4, kGWarps = 6;
-constexpr uint32_t kGABytes = kGM * 128, kGBBytes = kGN * 128, kGStageBytes = kGABytes + kGBBytes;
+// k-steps of 64, on pairs of CTAs: each holds the A rows of its 128 tokens and
+// half of B's columns, one tcgen05.mma of the leader multiplies both (the tensor
+// cores read their shared-memory operands at about 64 bytes a clock and SM; alone,
+// a CTA's 128 x 256 tile needs 96 for the full rate).  A pair walks its units (K
+// split, token tile, column tile); in each CTA warp 0 issues the copies, which
+// count on the leader's barrier, warp 1 of the leader the MMAs, warps 2-5 empty
+// one of two TMEM accumulators while the next fills.
+constexpr int kGM = 256, kGN = 256, kGStages = 6, kGWarps = 6;
+constexpr uint32_t kGABytes = kGM / 2 * 128, kGBBytes = kGN / 2 * 128, kGStageBytes = kGABytes + kGBBytes;
 constexpr uint32_t kGBarOff = kGStages * kGStageBytes;
 constexpr uint32_t kGSmem = kGBarOff + 256 + 1024;
 constexpr uint32_t kGTmem = 512;
@@ -306,7 +310,9 @@ enum GemmMode { kSoftmax, kAccumulate, kFinish };
 
 struct GemmParams {
   int32_t M, N;                        // tokens; columns of this product
-  int32_t n_k, n_mt, n_nt, splits, n_units;
+  int32_t n_k, n_mt, splits;
+  int32_t n_full, n_half;              // units of 256 columns; of the last 128 or fewer
+  int32_t half0, half_pairs;           // pairs that take the half units
   uint32_t* status;
   const float* grad;                   // [M]
   const int32_t* targets;              // [M]
@@ -350,40 +356,59 @@ __device__ __forceinline__ bool g_wait(const GemmSmem& s, uint32_t bar, uint32_t
   return warp_wait(s.abort_flag, bar, parity, status);
 }
 
+// The i-th unit of a pair: first its share of the full ones (round robin), then
+// of the half ones.
 struct GemmUnit {
   int m, n, k0, k1, split;
+  int cols;     // 256 or 128, half of them in each CTA
 };
-__device__ __forceinline__ GemmUnit g_unit(const GemmParams& p, int u) {
-  GemmUnit r;
-  const int tiles = p.n_mt * p.n_nt;
-  r.split = u / tiles;
-  const int rest = u - r.split * tiles;
-  r.n = rest / p.n_mt;
-  r.m = rest - r.n * p.n_mt;
+__device__ __forceinline__ bool g_unit(const GemmParams& p, int pair, int pairs, int i, GemmUnit& r) {
+  int u = pair + i * pairs, n_full_t = p.N / kGN;
+  const int mine = (p.n_full - pair + pairs - 1) / pairs;
+  r.cols = kGN;
+  if (i >= mine) {
+    const int h = pair - p.half0 + (i - mine) * p.half_pairs;
+    if (pair < p.half0 || pair >= p.half0 + p.half_pairs || h >= p.n_half) return false;
+    r.split = h / p.n_mt;
+    r.m = h - r.split * p.n_mt;
+    r.n = n_full_t;
+    r.cols = kGN / 2;
+  } else {
+    if (p.n_half == 0 && p.N % kGN != 0) ++n_full_t;   // a last tile of more than 128 columns counts as full
+    const int tiles = p.n_mt * n_full_t;
+    r.split = u / tiles;
+    const int rest = u - r.split * tiles;
+    r.n = rest / p.n_mt;
+    r.m = rest - r.n * p.n_mt;
+  }
   r.k0 = static_cast<int>(static_cast<int64_t>(p.n_k) * r.split / p.splits);
   r.k1 = static_cast<int>(static_cast<int64_t>(p.n_k) * (r.split + 1) / p.splits);
-  return r;
+  return true;
 }
 
 template <GemmMode kMode>
-__device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtensorMap* ma, const CUtensorMap* mb) {
+__device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtensorMap* ma, const CUtensorMap* mb,
+                           int pair, int pairs, int rank) {
   int s = 0, issued = 0;
   uint32_t ph = 0;
   bool ok = true;
-  for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
-    const GemmUnit w = g_unit(p, u);
-    const int nb = (min(kGN, p.N - w.n * kGN) + 63) / 64;   // 64-column blocks of B (stored [K][columns])
+  GemmUnit w;
+  for (int i = 0; ok && g_unit(p, pair, pairs, i, w); ++i) {
+    const int n0 = w.n * kGN + rank * (w.cols / 2);
+    const int nb = w.cols / 128;   // 64-column boxes of B (stored [K][columns])
+    const uint32_t bytes = 2 * (kGABytes + (kMode == kSoftmax ? kGBBytes : nb * 8192u));   // of both CTAs
     for (int k = w.k0; k < w.k1; ++k) {
       ok = g_wait(sm, sm.empty + 8 * s, ph ^ 1u, p.status);
       if (!ok) break;
       if (elect_one()) {
-        const uint32_t bar = sm.full + 8 * s, a = sm.stages + s * kGStageBytes, b = a + kGABytes;
-        mbar_arrive_expect_tx(bar, kGABytes + (kMode == kSoftmax ? kGBBytes : nb * 8192u));
-        tma_load_2d(a, ma, k * 64, w.m * kGM, bar);
+        const uint32_t a = sm.stages + s * kGStageBytes, b = a + kGABytes;
+        const uint32_t bar = cluster_addr(sm.full + 8 * s, 0);   // the leader's
+        if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * s, bytes);
+        tma_load_2d_pair(a, ma, k * 64, w.m * kGM + rank * (kGM / 2), bar);
         if constexpr (kMode == kSoftmax) {
-          tma_load_2d(b, mb, k * 64, w.n * kGN, bar);
+          tma_load_2d_pair(b, mb, k * 64, n0, bar);
         } else {
-          for (int i = 0; i < nb; ++i) tma_load_2d(b + i * 8192u, mb, w.n * kGN + 64 * i, k * 64, bar);
+          for (int e = 0; e < nb; ++e) tma_load_2d_pair(b + e * 8192u, mb, n0 + 64 * e, k * 64, bar);
         }
       }
       __syncwarp();
@@ -394,8 +419,8 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
       }
     }
   }
-  if (!ok) {
-    // Copies still in flight land before the block's shared memory goes away.
+  if (!ok && rank == 0) {
+    // Copies still in flight land before the pair's shared memory goes away.
     const int back = min(issued, kGStages);
     for (int i = 1; i <= back; ++i) {
       const int at = issued - i;
@@ -408,31 +433,32 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
 // tcgen05.mma costs mostly the instructions that prepare its operands, so each
 // is an immediate offset from running values that advance by constants.
 template <GemmMode kMode>
-__device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base) {
+__device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int pair, int pairs) {
   constexpr bool kMn = kMode != kSoftmax;
   constexpr uint32_t kBStep = kMn ? 128u : 2u;   // descriptor units per K = 16
   constexpr uint32_t kStep = kGStageBytes >> 4;
+  constexpr uint32_t kDesc = tc_idesc_f16(kGM, kGN) | (kMn ? kTcIdescBmn : 0u);
+  constexpr uint32_t kHalfDesc = tc_idesc_f16(kGM, kGN / 2) | (kMn ? kTcIdescBmn : 0u);
   const uint64_t ad0 = smem_desc_k128(sm.stages);
   const uint64_t bd0 = kMn ? smem_desc_mn128(sm.stages + kGABytes, 8192u) : smem_desc_k128(sm.stages + kGABytes);
   uint64_t a = ad0, b = bd0;
   uint32_t full = sm.full, empty = sm.empty, ph = 0, aph = 1, d = tmem_base, accf = sm.accf, acce = sm.acce;
   int s = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
-    const GemmUnit w = g_unit(p, u);
+  GemmUnit w;
+  for (int i = 0; g_unit(p, pair, pairs, i, w); ++i) {
     if (!g_wait(sm, acce, aph, p.status)) return;
     tc_fence_after();
-    const int ncol = (min(kGN, p.N - w.n * kGN) + 15) & ~15;
-    const uint32_t idesc = tc_idesc_f16(kGM, ncol) | (kMn ? kTcIdescBmn : 0u);
+    const uint32_t idesc = w.cols == kGN ? kDesc : kHalfDesc;
     uint32_t acc = 0;
     for (int k = w.k0; k < w.k1; ++k) {
       if (!g_wait(sm, full, ph, p.status)) return;
       tc_fence_after();
       if (elect_one()) {
-        tc_mma_ss(d, a, b, idesc, acc);
-        tc_mma_ss(d, a + 2, b + kBStep, idesc, 1u);
-        tc_mma_ss(d, a + 4, b + 2 * kBStep, idesc, 1u);
-        tc_mma_ss(d, a + 6, b + 3 * kBStep, idesc, 1u);
-        tc_commit(empty);
+        tc_mma_ss_pair(d, a, b, idesc, acc);
+        tc_mma_ss_pair(d, a + 2, b + kBStep, idesc, 1u);
+        tc_mma_ss_pair(d, a + 4, b + 2 * kBStep, idesc, 1u);
+        tc_mma_ss_pair(d, a + 6, b + 3 * kBStep, idesc, 1u);
+        tc_commit_pair(empty);
       }
       __syncwarp();
       acc = 1;
@@ -450,7 +476,7 @@ __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tme
         empty += 8;
       }
     }
-    if (elect_one()) tc_commit(accf);
+    if (elect_one()) tc_commit_pair(accf);
     __syncwarp();
     // the other accumulator
     if (d == tmem_base) {
@@ -470,15 +496,15 @@ __device__ __forceinline__ float grad_nan() { return __int_as_float(0x7fc00000);
 
 // Lane = token row, columns in pieces of 32.
 template <GemmMode kMode>
-__device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int lane) {
+__device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int lane, int pair, int pairs,
+                           int rank) {
   const int q = (threadIdx.x >> 5) & 3;
   bool ok = true;
-  int i = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++i) {
-    const GemmUnit w = g_unit(p, u);
+  GemmUnit w;
+  for (int i = 0; g_unit(p, pair, pairs, i, w); ++i) {
     const uint32_t acc = i & 1;
-    const int t = w.m * kGM + 32 * q + lane, n0 = w.n * kGN;
-    const int ncol = min(kGN, p.N - n0);
+    const int t = w.m * kGM + rank * (kGM / 2) + 32 * q + lane, n0 = w.n * kGN;
+    const int ncol = min(w.cols, p.N - n0);
     const bool live = t < p.M;
     float g = 0.f, cinv = 0.f, lse = 0.f;
     int target = -1;
@@ -582,12 +608,12 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
       tc_fence_before();
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(sm.acce + 8 * acc);
+    if (lane == 0) mbar_arrive_cluster(cluster_addr(sm.acce + 8 * acc, 0));
   }
 }
 
 template <GemmMode kMode>
-__global__ void __launch_bounds__(kGWarps * 32, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGWarps * 32, 1)
     grad_gemm_kernel(const GemmParams p, const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -600,6 +626,7 @@ __global__ void __launch_bounds__(kGWarps * 32, 1)
   sm.tmem = reinterpret_cast<uint32_t*>(base + kGBarOff + 16 * kGStages + 32);
   sm.abort_flag = reinterpret_cast<int*>(sm.tmem + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, rank = blockIdx.x & 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGStages; ++s) {
       mbar_init(sm.full + 8 * s, 1);
@@ -607,36 +634,50 @@ __global__ void __launch_bounds__(kGWarps * 32, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(sm.accf + 8 * a, 1);
-      mbar_init(sm.acce + 8 * a, 4);
+      mbar_init(sm.acce + 8 * a, 8);   // the epilogue warps of both CTAs
     }
     *sm.abort_flag = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_addr(sm.tmem), kGTmem);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_addr(sm.tmem), kGTmem);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *sm.tmem;
-  if (warp == 0) g_tma_warp<kMode>(p, sm, &ma, &mb);
-  else if (warp == 1) g_mma_warp<kMode>(p, sm, tmem_base);
-  else g_epilogue<kMode>(p, sm, tmem_base, lane);
+  if (warp == 0) g_tma_warp<kMode>(p, sm, &ma, &mb, pair, pairs, rank);
+  else if (warp == 1) {
+    if (rank == 0) g_mma_warp<kMode>(p, sm, tmem_base, pair, pairs);
+  } else g_epilogue<kMode>(p, sm, tmem_base, lane, pair, pairs, rank);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // nothing of the pair still reads, writes or signals the other CTA
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kGTmem);
+    tmem_dealloc_pair(tmem_base, kGTmem);
   }
 }
 
 template <GemmMode kMode>
 cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap& mb, int num_sms, cudaStream_t stream) {
+  const int rest = p.N % kGN, pairs = num_sms / 2;
+  const bool half = rest != 0 && rest <= kGN / 2;
   p.n_mt = (p.M + kGM - 1) / kGM;
-  p.n_nt = (p.N + kGN - 1) / kGN;
-  p.n_units = p.splits * p.n_mt * p.n_nt;
-  grad_gemm_kernel<kMode><<<std::min(p.n_units, num_sms), kGWarps * 32, kGSmem, stream>>>(p, ma, mb);
+  p.n_full = p.splits * p.n_mt * (p.N / kGN + (rest != 0 && !half ? 1 : 0));
+  p.n_half = half ? p.splits * p.n_mt : 0;
+  const int grid = std::min(p.n_full + p.n_half, pairs);
+  // The half units go to the pairs that the last round of full ones leaves idle,
+  // two each, if they fit there; else to all.
+  p.half0 = p.n_full % grid;
+  p.half_pairs = grid - p.half0;
+  if (p.n_half > 2 * p.half_pairs) {
+    p.half0 = 0;
+    p.half_pairs = grid;
+  }
+  grad_gemm_kernel<kMode><<<2 * grid, kGWarps * 32, kGSmem, stream>>>(p, ma, mb);
   return cudaGetLastError();
 }
 
@@ -1152,7 +1193,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     // Few tiles: the accumulation splits its K (the rows of a chunk) so that
     // every SM has a unit; the splits are added in order at the end.
     const int tiles = ((o.tokens + kGM - 1) / kGM) * ((Kc + kGN - 1) / kGN);
-    o.splits = std::max(1, std::min(h.num_sms / tiles, o.chunk / 256));
+    o.splits = std::max(1, std::min(h.num_sms / 2 / tiles, o.chunk / 256));
     o.cinv = take(t * 4);
     o.xop = take(t * Kc * 2);
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
@@ -1275,7 +1316,7 @@ int grad_finish(const GradCall& c, GemmParams& p, int splits, int splits_small, 
   cudaError_t e = cudaGetLastError();
   CUtensorMap mz{}, mr{};
   if (e == cudaSuccess && Kz > 0) {
-    e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM);
+    e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM / 2);
     if (e == cudaSuccess) e = tc_encode_map(&mr, reinterpret_cast<const uint16_t*>(c.wb + c.o.rb), L.d, Kz, L.d, 64);
   }
   if (e != cudaSuccess) return set_cuda_error(e);
@@ -1345,9 +1386,9 @@ int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
     const int64_t items = static_cast<int64_t>(dq.n_mt) * dq.n_ks;
     dequant_rows_kernel<<<static_cast<unsigned>((items + 7) / 8), 256, 0, c.stream>>>(dq);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = tc_encode_map(&mx, xop, Kc, nt, Kc, kGM);
-    if (e == cudaSuccess) e = tc_encode_map(&mg, p.G, rows, nt, o.pitch, kGM);
-    if (e == cudaSuccess) e = tc_encode_map(&mwk, w, Kc, rows, Kc, kGN);
+    if (e == cudaSuccess) e = tc_encode_map(&mx, xop, Kc, nt, Kc, kGM / 2);
+    if (e == cudaSuccess) e = tc_encode_map(&mg, p.G, rows, nt, o.pitch, kGM / 2);
+    if (e == cudaSuccess) e = tc_encode_map(&mwk, w, Kc, rows, Kc, kGN / 2);
     if (e == cudaSuccess) e = tc_encode_map(&mwn, w, Kc, rows, Kc, 64);
     if (e != cudaSuccess) return set_cuda_error(e);
     p.v0 = v0;
