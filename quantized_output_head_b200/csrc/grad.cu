@@ -18,7 +18,7 @@
 //   sum_v (exp(y - lse) / S - [v = target]) W[v] = (G W) / S + (1/S - 1) W[target].
 // (On a vocabulary shard S is not known and lse is taken as it is.)
 //
-// The vocabulary is walked in chunks of at most kGradChunk rows.  Per chunk
+// Many tokens: the vocabulary is walked in chunks of rows.  Per chunk
 //   1. dequant_rows_kernel   W~ of the chunk, fp16, in the workspace
 //   2. gemm softmax          G of the chunk, fp16
 //   3. gemm accumulate       dX += G W~, fp32
@@ -47,8 +47,11 @@ namespace archead {
 
 namespace {
 
-constexpr int kGradChunk = 16384;     // vocabulary rows of one pass (W~ chunk: 153 MB at 4672 columns)
 constexpr int kGradTokens = 4096;     // tokens of one pass over the head
+// Vocabulary rows of one pass: as many as keep the W~ chunk and the G chunk near
+// these sizes (16,640 rows at 4096 tokens and 4672 columns; fewer passes re-read
+// and re-write dX less often, and leave fewer part-filled rounds of tiles).
+constexpr size_t kGradWBytes = size_t(160) << 20, kGradGBytes = size_t(256) << 20;
 constexpr int kGradScale = 15;        // G is stored times 2^15
 
 // ------------------------------------------------------------ packed -> fp16
@@ -303,7 +306,8 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
 constexpr int kGM = 256, kGN = 256, kGStages = 6, kGWarps = 6;
 constexpr uint32_t kGABytes = kGM / 2 * 128, kGBBytes = kGN / 2 * 128, kGStageBytes = kGABytes + kGBBytes;
 constexpr uint32_t kGBarOff = kGStages * kGStageBytes;
-constexpr uint32_t kGSmem = kGBarOff + 256 + 1024;
+constexpr uint32_t kGTileOff = kGBarOff + 256;       // [4] 32 x 33 words, one per epilogue warp
+constexpr uint32_t kGSmem = kGTileOff + 4 * 32 * 33 * 4 + 1024;
 constexpr uint32_t kGTmem = 512;
 
 enum GemmMode { kSoftmax, kAccumulate, kFinish };
@@ -337,6 +341,7 @@ struct GemmSmem {
   uint32_t stages, full, empty, accf, acce;   // addresses
   uint32_t* tmem;
   int* abort_flag;
+  uint32_t* tile;
 };
 
 __device__ __forceinline__ bool aborted(int* flag) { return *reinterpret_cast<volatile int*>(flag) != 0; }
@@ -494,17 +499,20 @@ __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tme
 
 __device__ __forceinline__ float grad_nan() { return __int_as_float(0x7fc00000); }
 
-// Lane = token row, columns in pieces of 32.
+// Columns in pieces of 32.  A lane holds one token's row of the accumulator; G
+// and dX cross the warp through a padded tile, so that a load or store touches a
+// few whole row segments and not 16 bytes of 32 rows.
 template <GemmMode kMode>
 __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int lane, int pair, int pairs,
                            int rank) {
   const int q = (threadIdx.x >> 5) & 3;
+  uint32_t* tile = sm.tile + q * (32 * 33);
   bool ok = true;
   GemmUnit w;
   for (int i = 0; g_unit(p, pair, pairs, i, w); ++i) {
     const uint32_t acc = i & 1;
-    const int t = w.m * kGM + rank * (kGM / 2) + 32 * q + lane, n0 = w.n * kGN;
-    const int ncol = min(w.cols, p.N - n0);
+    const int t0 = w.m * kGM + rank * (kGM / 2) + 32 * q, t = t0 + lane, n0 = w.n * kGN;
+    const int ncol = min(w.cols, p.N - n0), nrow = min(32, p.M - t0);
     const bool live = t < p.M;
     float g = 0.f, cinv = 0.f, lse = 0.f;
     int target = -1;
@@ -517,7 +525,7 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
       }
     }
     if (ok) ok = g_wait(sm, sm.accf + 8 * acc, (i >> 1) & 1, p.status);
-    if (ok) {
+    if (ok && nrow > 0) {
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * kGN;
       if constexpr (kMode == kFinish) {
@@ -531,13 +539,10 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + c0, r);
         tmem_ld_wait();
-        if (!live) {
-          // a row past the last token
-        } else if constexpr (kMode == kSoftmax) {
+        if constexpr (kMode == kSoftmax) {
           // columns are vocabulary rows of the chunk; a token without a
           // gradient gets zeros (its lse and target may be anything)
           const int tl = target - p.row0 - p.v0 - n0 - c0;
-          uint32_t o[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             float e[2];
@@ -548,57 +553,73 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
               ssum += x;
               e[h] = (x - (g != 0.f && c + h == tl ? 1.f : 0.f)) * static_cast<float>(1 << kGradScale);
             }
-            o[c / 2] = pack_half2(e[0], e[1]);
+            tile[lane * 17 + c / 2] = pack_half2(e[0], e[1]);
           }
-          uint4* dst = reinterpret_cast<uint4*>(p.G + static_cast<size_t>(t) * p.pitch + n0 + c0);
+          __syncwarp();
+          // 16-byte runs: four of a row's 64 bytes, eight rows at a time
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (c0 + 8 * v < ncol) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-        } else if constexpr (kMode == kAccumulate) {
-          float4* dst = reinterpret_cast<float4*>(p.dx + w.split * p.split_stride + static_cast<size_t>(t) * p.Kc + n0 + c0);
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            float4 x = make_float4(__uint_as_float(r[4 * v]), __uint_as_float(r[4 * v + 1]),
-                                   __uint_as_float(r[4 * v + 2]), __uint_as_float(r[4 * v + 3]));
-            if (w.k0 == w.k1) x = make_float4(0.f, 0.f, 0.f, 0.f);   // a split without rows in a short chunk
-            if (!p.first) {
-              const float4 y = dst[v];
-              x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+          for (int it = 0; it < 4; ++it) {
+            const int row = 8 * it + (lane >> 2), v = lane & 3;
+            if (row < nrow && c0 + 8 * v < ncol) {
+              const uint32_t* src = tile + row * 17 + 4 * v;
+              *reinterpret_cast<uint4*>(p.G + static_cast<size_t>(t0 + row) * p.pitch + n0 + c0 + 8 * v) =
+                  make_uint4(src[0], src[1], src[2], src[3]);
             }
-            dst[v] = x;
+          }
+        } else if constexpr (kMode == kAccumulate) {
+          const bool none = w.k0 == w.k1;   // a split without rows in a short chunk
+#pragma unroll
+          for (int c = 0; c < 32; ++c) tile[lane * 33 + c] = none ? 0u : r[c];
+          __syncwarp();
+          float* dst = p.dx + w.split * p.split_stride + static_cast<size_t>(t0) * p.Kc + n0 + c0 + lane;
+          float old[32];
+          if (!p.first) {
+#pragma unroll
+            for (int row = 0; row < 32; ++row) old[row] = row < nrow ? dst[static_cast<size_t>(row) * p.Kc] : 0.f;
+          }
+#pragma unroll
+          for (int row = 0; row < 32; ++row) {
+            if (row < nrow) {
+              const float x = __uint_as_float(tile[row * 33 + lane]);
+              dst[static_cast<size_t>(row) * p.Kc] = p.first ? x : old[row] + x;
+            }
           }
         } else {
-          float x[32];
+          if (live) {
+            // row segments of 128 bytes and more, lane by lane (through the tile
+            // this took half as long again: both ways cross it)
+            float x[32];
+            const float4* src = reinterpret_cast<const float4*>(p.dx + static_cast<size_t>(t) * p.Kc + n0 + c0);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = p.n_k > 0 ? __uint_as_float(r[c]) * p.mul_acc : 0.f;
-          const float4* src = reinterpret_cast<const float4*>(p.dx + static_cast<size_t>(t) * p.Kc + n0 + c0);
+            for (int c = 0; c < 32; ++c) x[c] = p.n_k > 0 ? __uint_as_float(r[c]) * p.mul_acc : 0.f;
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const float4 y = src[v];
-            const float z[4] = {y.x, y.y, y.z, y.w};
+            for (int v = 0; v < 8; ++v) {
+              const float4 y = src[v];
+              const float z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = 4 * v + e, c = (at & 16) + tc_kcol(at & 15);
-              x[c] = fmaf(z[e], p.mul_dx, x[c]);
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = g == 0.f ? 0.f : x[c] * g;
-          if (p.out_f32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + static_cast<size_t>(t) * p.N + n0 + c0);
-#pragma unroll
-            for (int v = 0; v < 8; ++v) dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(t) * p.N + n0 + c0);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t o[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * v + 2 * e], x[8 * v + 2 * e + 1]);
-                o[e] = *reinterpret_cast<const uint32_t*>(&b);
+              for (int e = 0; e < 4; ++e) {   // dX is in the operand order
+                const int at = 4 * v + e, c = (at & 16) + tc_kcol(at & 15);
+                x[c] = fmaf(z[e], p.mul_dx, x[c]);
               }
-              dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = g == 0.f ? 0.f : x[c] * g;
+            if (p.out_f32) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + static_cast<size_t>(t) * p.N + n0 + c0);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<size_t>(t) * p.N + n0 + c0);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * v + 2 * e], x[8 * v + 2 * e + 1]);
+                  o[e] = *reinterpret_cast<const uint32_t*>(&b);
+                }
+                dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
+              }
             }
           }
         }
@@ -625,6 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGWarps * 32, 1)
   sm.acce = sm.accf + 16;
   sm.tmem = reinterpret_cast<uint32_t*>(base + kGBarOff + 16 * kGStages + 32);
   sm.abort_flag = reinterpret_cast<int*>(sm.tmem + 1);
+  sm.tile = reinterpret_cast<uint32_t*>(base + kGTileOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2, rank = blockIdx.x & 1;
   if (threadIdx.x == 0) {
@@ -1186,9 +1208,10 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     const GwPlan g = gw_plan(h);
     o.splits = std::max(g.s_big, g.s_small);
   } else {
-    const int n_chunks = (L.Vp + kGradChunk - 1) / kGradChunk;
+    const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * t)));
+    const int n_chunks = static_cast<int>((L.Vp + rows - 1) / rows);
     o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
-    o.pitch = o.chunk;
+    o.pitch = o.chunk + 64;   // (a power of two between G's rows would send a whole box to one memory channel)
     o.n_ssum = (L.Vp + kGN - 1) / kGN;
     // Few tiles: the accumulation splits its K (the rows of a chunk) so that
     // every SM has a unit; the splits are added in order at the end.
