@@ -301,13 +301,13 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
 // cores read their shared-memory operands at about 64 bytes a clock and SM; alone,
 // a CTA's 128 x 256 tile needs 96 for the full rate).  A pair walks its units (K
 // split, token tile, column tile); in each CTA warp 0 issues the copies, which
-// count on the leader's barrier, warp 1 of the leader the MMAs, warps 2-5 empty
+// count on the leader's barrier, warp 1 of the leader the MMAs, warps 2-9 empty
 // one of two TMEM accumulators while the next fills.
-constexpr int kGM = 256, kGN = 256, kGStages = 6, kGWarps = 6;
+constexpr int kGM = 256, kGN = 256, kGStages = 6, kGEpi = 8, kGWarps = 2 + kGEpi;
 constexpr uint32_t kGABytes = kGM / 2 * 128, kGBBytes = kGN / 2 * 128, kGStageBytes = kGABytes + kGBBytes;
 constexpr uint32_t kGBarOff = kGStages * kGStageBytes;
-constexpr uint32_t kGTileOff = kGBarOff + 256;       // [4] 32 x 33 words, one per epilogue warp
-constexpr uint32_t kGSmem = kGTileOff + 4 * 32 * 33 * 4 + 1024;
+constexpr uint32_t kGTileOff = kGBarOff + 256;       // 32 x 33 words per epilogue warp
+constexpr uint32_t kGSmem = kGTileOff + kGEpi * 32 * 33 * 4 + 1024;
 constexpr uint32_t kGTmem = 512;
 
 enum GemmMode { kSoftmax, kAccumulate, kFinish };
@@ -326,7 +326,7 @@ struct GemmParams {
   const float* lse;                    // [M]
   uint16_t* G;                         // [M][pitch]
   int32_t pitch, v0, V;                // first row of the chunk, rows of the head
-  float* ssum;                         // [tiles][tokens]: sums of exp(y - lse) over the tile's rows
+  float* ssum;                         // [tiles][2][tokens]: sums of exp(y - lse) over half a tile's rows
   int32_t tokens;
   // accumulate / finish
   float* dx;                           // [splits][M][Kc]
@@ -497,6 +497,11 @@ __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tme
   }
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float grad_nan() { return __int_as_float(0x7fc00000); }
 
 // Columns in pieces of 32.  A lane holds one token's row of the accumulator; G
@@ -505,14 +510,14 @@ __device__ __forceinline__ float grad_nan() { return __int_as_float(0x7fc00000);
 template <GemmMode kMode>
 __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int lane, int pair, int pairs,
                            int rank) {
-  const int q = (threadIdx.x >> 5) & 3;
-  uint32_t* tile = sm.tile + q * (32 * 33);
+  const int ew = (threadIdx.x >> 5) - 2, q = (ew + 2) & 3, half = ew >> 2;   // TMEM lane quarter, half of the columns
+  uint32_t* tile = sm.tile + ew * (32 * 33);
   bool ok = true;
   GemmUnit w;
   for (int i = 0; g_unit(p, pair, pairs, i, w); ++i) {
     const uint32_t acc = i & 1;
     const int t0 = w.m * kGM + rank * (kGM / 2) + 32 * q, t = t0 + lane, n0 = w.n * kGN;
-    const int ncol = min(w.cols, p.N - n0), nrow = min(32, p.M - t0);
+    const int ncol = min((half + 1) * (w.cols / 2), p.N - n0), nrow = min(32, p.M - t0);
     const bool live = t < p.M;
     float g = 0.f, cinv = 0.f, lse = 0.f;
     int target = -1;
@@ -534,27 +539,37 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
           if (w.n == 0) atomicOr(p.status, static_cast<uint32_t>(ARCHEAD_STATUS_BAD_TARGET));
         }
       }
+      // probabilities come out of the exponential times 2^15
+      const float k2 = cinv * 1.44269504f, l2 = lse * 1.44269504f - static_cast<float>(kGradScale);
       float ssum = 0.f;
-      for (int c0 = 0; c0 < ncol; c0 += 32) {
+      for (int c0 = half * (w.cols / 2); c0 < ncol; c0 += 32) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(taddr + c0, r);
         tmem_ld_wait();
         if constexpr (kMode == kSoftmax) {
           // columns are vocabulary rows of the chunk; a token without a
           // gradient gets zeros (its lse and target may be anything)
-          const int tl = target - p.row0 - p.v0 - n0 - c0;
+          const int tl = target - p.row0 - p.v0 - n0 - c0, left = p.V - p.v0 - n0 - c0;
+          float x[32];
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            float e[2];
+          for (int c = 0; c < 32; ++c) x[c] = exp2_approx(fmaf(__uint_as_float(r[c]), k2, -l2));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float x = __expf(fmaf(__uint_as_float(r[c + h]), cinv, -lse));
-              if (g == 0.f || p.v0 + n0 + c0 + c + h >= p.V) x = 0.f;
-              ssum += x;
-              e[h] = (x - (g != 0.f && c + h == tl ? 1.f : 0.f)) * static_cast<float>(1 << kGradScale);
-            }
-            tile[lane * 17 + c / 2] = pack_half2(e[0], e[1]);
+          for (int c = 0; c < 32; ++c)
+            if (g == 0.f) x[c] = 0.f;
+          if (left < 32) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= left) x[c] = 0.f;
           }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) ssum += (x[c] + x[c + 1]) + (x[c + 2] + x[c + 3]);
+          if (__any_sync(0xffffffffu, g != 0.f && tl >= 0 && tl < 32)) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (g != 0.f && c == tl) x[c] -= static_cast<float>(1 << kGradScale);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) tile[lane * 17 + c / 2] = pack_half2(x[c], x[c + 1]);
           __syncwarp();
           // 16-byte runs: four of a row's 64 bytes, eight rows at a time
 #pragma unroll
@@ -625,7 +640,8 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
         }
         __syncwarp();
       }
-      if (kMode == kSoftmax && live) p.ssum[static_cast<size_t>(p.v0 / kGN + w.n) * p.tokens + t] = ssum;
+      if (kMode == kSoftmax && live)
+        p.ssum[static_cast<size_t>(2 * (p.v0 / kGN + w.n) + half) * p.tokens + t] = ssum * (1.f / (1 << kGradScale));
       tc_fence_before();
     }
     __syncwarp();
@@ -656,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGWarps * 32, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(sm.accf + 8 * a, 1);
-      mbar_init(sm.acce + 8 * a, 8);   // the epilogue warps of both CTAs
+      mbar_init(sm.acce + 8 * a, 2 * kGEpi);   // the epilogue warps of both CTAs
     }
     *sm.abort_flag = 0;
     mbar_fence_init();
@@ -1178,6 +1194,27 @@ GwPlan gw_plan(const archead_handle& h) {
   return g;
 }
 
+// K splits (of a chunk's rows) of the accumulation: the fewest that keep the
+// pairs busy.  Rounds of units over the pairs, a last column tile of 128 or fewer
+// being half a unit, per split; each further split has to save 3% for its
+// partial dX.
+int accumulate_splits(int tokens, int Kc, int chunk, int pairs) {
+  const int mt = (tokens + kGM - 1) / kGM, rest = Kc % kGN;
+  const bool half = rest != 0 && rest <= kGN / 2;
+  const int full1 = mt * (Kc / kGN + (rest != 0 && !half ? 1 : 0)), half1 = half ? mt : 0;
+  int best = 1;
+  double best_cost = 1e30;
+  for (int s = 1; s <= 8 && s * 256 <= chunk; ++s) {
+    const int full = s * full1, rounds = (full + pairs - 1) / pairs, idle = rounds * pairs - full;
+    const double cost = (rounds + (s * half1 > 2 * idle ? 0.5 : 0.0)) / s * (1.0 + 0.03 * (s - 1));
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 struct GradLayout {
   bool few;
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
@@ -1212,11 +1249,8 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     const int n_chunks = static_cast<int>((L.Vp + rows - 1) / rows);
     o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
     o.pitch = o.chunk + 64;   // (a power of two between G's rows would send a whole box to one memory channel)
-    o.n_ssum = (L.Vp + kGN - 1) / kGN;
-    // Few tiles: the accumulation splits its K (the rows of a chunk) so that
-    // every SM has a unit; the splits are added in order at the end.
-    const int tiles = ((o.tokens + kGM - 1) / kGM) * ((Kc + kGN - 1) / kGN);
-    o.splits = std::max(1, std::min(h.num_sms / 2 / tiles, o.chunk / 256));
+    o.n_ssum = 2 * ((L.Vp + kGN - 1) / kGN);
+    o.splits = accumulate_splits(o.tokens, Kc, o.chunk, h.num_sms / 2);
     o.cinv = take(t * 4);
     o.xop = take(t * Kc * 2);
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
