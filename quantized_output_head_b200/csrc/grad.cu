@@ -65,7 +65,12 @@ struct DequantParams {
 };
 
 __device__ __forceinline__ uint32_t ldg32(const uint8_t* p) { return __ldg(reinterpret_cast<const uint32_t*>(p)); }
-__device__ __forceinline__ uint4 ldg128(const uint8_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+// (Packed codes are read once: they take no line of L1.)
+__device__ __forceinline__ uint4 ldg128(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // Scale pair (rows gr, gr + 8) times 2^e, as two half2 (s, s).
 __device__ __forceinline__ void scales_of(uint32_t bits, float mul, uint32_t& s0, uint32_t& s1) {
@@ -778,12 +783,14 @@ __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
 //   warps 0-15  dequantise: set w / 4 takes every fourth tile, a warp two 16-row
 //               m-tiles of it, their packed bytes loaded one of its tiles
 //               early straight into registers (one 16-byte load per lane and 64
-//               columns: nothing to copy, wait for or re-read).  They also bring
-//               G: warp w the 32 tokens of its TMEM lane quarter w % 4, 32
-//               columns of each k-step.
-//   warp 16     MMA
+//               columns: nothing to copy, wait for or re-read).
+//   warps 16-19 G: the 32 tokens of their TMEM lane quarter, a k-step ahead in
+//               registers; warp 19 also issues the MMAs (as a duty of warps 0-15
+//               G cost the schedulers of the first quarters two thirds more
+//               instructions than the others).
 // Afterwards warps 0-15 write the accumulators.
-constexpr int kGwWarps = 17, kGwSets = 4, kGwStages = 6, kGwBlocks = 3, kGwBufs = 2;
+constexpr int kGwWarps = 20, kGwSets = 4, kGwStages = 4, kGwBlocks = 3, kGwBufs = 2;
+constexpr int kGwMma = kGwWarps - 1;                  // the warp that issues the MMAs
 constexpr uint32_t kGwHalf = kGwRows * 128;           // 128 rows x 64 columns of fp16
 constexpr uint32_t kGwTile = 2 * kGwHalf;
 constexpr uint32_t kGwBarOff = kGwStages * kGwTile;
@@ -906,14 +913,14 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
       mbar_init(wempty + 8 * s, 1);
     }
     for (int s = 0; s < kGwBufs; ++s) {
-      mbar_init(gfull + 8 * s, 4 * ((p.T + 31) / 32));
+      mbar_init(gfull + 8 * s, (p.T + 31) / 32);
       mbar_init(gempty + 8 * s, 1);
     }
     mbar_init(done, 1);
     *flag = 0;
     mbar_fence_init();
   }
-  if (warp == 16) {
+  if (warp == kGwMma) {
     tmem_alloc(smem_addr(tmem), kGTmem);
     tmem_relinquish();
   }
@@ -941,7 +948,6 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
     // byte offsets of this lane inside a tile: row 16 j + gr (and 64 below), 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
     const uint32_t row = tiles + static_cast<uint32_t>((16 * j + gr) * 128);
     const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16), o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
-    bool ok = true;
     // the ring stage of this set's next tile
     int s = set;
     uint32_t ph = 1;
@@ -955,43 +961,6 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
         ph ^= 1u;
       }
     };
-
-    // G: token 32 j + lane, columns 32 set .. + 31 of each k-step, loaded one
-    // k-step ahead and stored when this warp reaches the k-step.
-    const bool has_g = 32 * j < p.T;
-    const int nq = (p.T + 31) / 32;
-    const uint4* gsrc = p.G + (static_cast<size_t>(k0) * nq + j) * (kGwRows / 8 * 32) + 4 * set * 32 + lane;
-    const uint32_t gdst = tbase + (static_cast<uint32_t>(32 * j) << 16) + 128 * kGwBlocks + 16 * set;
-    int gi = 0;
-    uint32_t gv[16];
-    auto g_load = [&]() {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) gv[i] = 0u;
-      if (has_g && gi < steps) {
-        const uint4* src = gsrc + static_cast<size_t>(gi) * nq * (kGwRows / 8 * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = __ldg(src + 32 * i);
-          gv[4 * i] = x.x; gv[4 * i + 1] = x.y; gv[4 * i + 2] = x.z; gv[4 * i + 3] = x.w;
-        }
-      }
-    };
-    auto g_until = [&](int last) {   // (a warp without tokens has nothing to bring)
-      while (has_g && ok && gi <= last && gi < steps) {
-        const int q = gi & (kGwBufs - 1);
-        ok = warp_wait(flag, gempty + 8 * q, ((gi / kGwBufs) & 1) ^ 1, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        tmem_st_32x32b_x16(gdst + (kGwRows / 2) * q, gv);
-        ++gi;
-        g_load();
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(gfull + 8 * q);
-      }
-    };
-    g_load();
 
     // The next tile's packed bytes, both m-tiles.  Every load has its own
     // register and at most a predicate: a load under a branch that others share a
@@ -1044,9 +1013,7 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
         b -= nbl;
         ++k;
       }
-      g_until(k - k0);
-      if (ok) ok = warp_wait(flag, wempty + 8 * s, ph, p.status);
-      if (!ok) break;
+      if (!warp_wait(flag, wempty + 8 * s, ph, p.status)) break;
       const int c = c0 + cstep * b;
       pb += kGwSets;
       aim();
@@ -1072,11 +1039,10 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
       filled();
       b += kGwSets;
     }
-    g_until(steps);
     // The accumulators: lane quarter w % 4 (tokens), every fourth piece of 32
     // columns.  A lane's 32 columns are two runs of the dequantising lanes' 16:
     // float4 (h, st) of them is operand columns 16 st + 4 (2 half + h) of the chunk.
-    if (warp_wait(flag, done, 0u, p.status) && has_g) {
+    if (warp_wait(flag, done, 0u, p.status) && 32 * j < p.T) {
       tc_fence_after();
       const int t = 32 * j + lane;
       float* dx = p.dx + split * p.split_stride + static_cast<size_t>(t) * p.rows.Kc;
@@ -1101,6 +1067,45 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
       tc_fence_before();
     }
   } else {
+    // G of this warp's 32 tokens: 128 rows of a k-step are 16 runs of 8, one
+    // 16-byte load each, 64 TMEM columns.
+    const int q = warp & 3;
+    const bool has_g = 32 * q < p.T;
+    const int nq = (p.T + 31) / 32;
+    const uint4* gsrc = p.G + (static_cast<size_t>(k0) * nq + q) * (kGwRows / 8 * 32) + lane;
+    const uint32_t gdst = tbase + (static_cast<uint32_t>(32 * q) << 16) + 128 * kGwBlocks;
+    int gi = 0;
+    uint32_t gv[4][16];
+    auto g_load = [&]() {
+      if (gi < steps) {
+        const uint4* src = gsrc + static_cast<size_t>(gi) * nq * (kGwRows / 8 * 32);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint4 x = __ldg(src + 32 * i);
+          uint32_t* v = &gv[i >> 2][4 * (i & 3)];
+          v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        }
+      }
+    };
+    auto g_put = [&]() {   // k-step gi
+      const int s = gi & (kGwBufs - 1);
+      if (!warp_wait(flag, gempty + 8 * s, ((gi / kGwBufs) & 1) ^ 1, p.status)) return false;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_st_32x32b_x16(gdst + (kGwRows / 2) * s + 16 * i, gv[i]);
+      ++gi;
+      g_load();
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(gfull + 8 * s);
+      return true;
+    };
+    if (has_g) g_load();
+    if (warp != kGwMma) {
+      if (has_g)
+        while (gi < steps && g_put()) {}
+    } else {
     // (running values and immediate offsets only, as in g_mma_warp)
     const uint64_t bd0 = smem_desc_mn128(tiles, kGwHalf);
     constexpr uint32_t kFull = tc_idesc_f16(128, 128) | kTcIdescBmn;
@@ -1109,8 +1114,8 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
     const uint32_t a0 = tbase + 128 * kGwBlocks;
     uint64_t bd = bd0;
     uint32_t ad = a0, wf = wfull, we = wempty, wph = 0, gf = gfull, ge = gempty, gph = 0;
-    bool ok = true;
     uint32_t acc = 0;
+    bool ok = !has_g || g_put();
     for (int k = 0; k < steps && ok; ++k) {
       ok = warp_wait(flag, gf, gph, p.status);
       if (!ok) break;
@@ -1144,6 +1149,9 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
           we = wempty;
           wph ^= 1u;
         }
+        // its own share of the next k-step, when this one's first MMAs are queued
+        if (b == 0 && has_g && gi < steps) ok = g_put();
+        if (!ok) break;
       }
       acc = 1;
       ad += kGwRows / 2;
@@ -1158,10 +1166,11 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
     }
     if (ok && elect_one()) tc_commit(done);
     __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kGwMma) {
     tc_fence_after();
     tmem_dealloc(tbase, kGTmem);
   }
