@@ -34,11 +34,20 @@ int check_device(const archead_handle* h) {
   return dev == h->device ? ARCHEAD_OK : ARCHEAD_EINVAL;
 }
 
+// What a gradient call takes from the tensor-core kernel in place of the forward's outputs.
+struct TcGradArgs {
+  const float* lse;
+  const float* grad;
+  const int32_t* targets;
+  void* G;
+  float* ssum;
+};
+
 // Tensor-core path: activation operand, the tensor-core kernel, and the
 // per-token fold of its partials.
 int forward_tc(const archead_handle* h, const uint16_t* hidden, int32_t T, const int32_t* targets, float* logits,
                int32_t* argmax, float* lse, float* ce, float4* shard_out, uint8_t* wb, const WsLayout& w,
-               cudaStream_t stream) {
+               cudaStream_t stream, const TcGradArgs* grad = nullptr) {
   const Layout& L = h->L;
   const int Kc = tc_kc(L);
   uint32_t* status = reinterpret_cast<uint32_t*>(wb + w.status);
@@ -101,6 +110,13 @@ int forward_tc(const archead_handle* h, const uint16_t* hidden, int32_t T, const
   tp.sc_res = std::ldexp(1.f, h->tc_alpha);
   tp.sc_L = std::ldexp(1.f, h->tc_beta);
   tp.sc_A = std::ldexp(1.f, h->tc_gamma);
+  if (grad != nullptr) {
+    tp.targets = grad->targets;
+    tp.lse = grad->lse;
+    tp.grad = grad->grad;
+    tp.G = static_cast<uint4*>(grad->G);
+    tp.ssum = grad->ssum;
+  }
   tc_smem_plan(tp);
   CUtensorMap map;
   e = tc_encode_xmap(&map, xop, T, Kc, tp.BN);
@@ -261,6 +277,15 @@ int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float
   archead_handle q = h;
   q.ev_before = q.ev_after = nullptr;
   return forward(&q, hidden, T, nullptr, logits, nullptr, nullptr, nullptr, ws, ws_bytes, stream);
+}
+
+int forward_tc_grad(const archead_handle& h, const uint16_t* hidden, int T, const int32_t* targets, const float* lse,
+                    const float* grad, void* G, float* ssum, void* ws, cudaStream_t stream) {
+  archead_handle q = h;
+  q.ev_before = q.ev_after = nullptr;
+  const TcGradArgs ga{lse, grad, targets, G, ssum};
+  return forward_tc(&q, hidden, T, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, static_cast<uint8_t*>(ws),
+                    ws_layout(q, T), stream, &ga);
 }
 
 int set_cuda_error(cudaError_t e) {

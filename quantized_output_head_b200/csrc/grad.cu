@@ -52,7 +52,7 @@ constexpr int kGradTokens = 4096;     // tokens of one pass over the head
 // these sizes (16,640 rows at 4096 tokens and 4672 columns; fewer passes re-read
 // and re-write dX less often, and leave fewer part-filled rounds of tiles).
 constexpr size_t kGradWBytes = size_t(160) << 20, kGradGBytes = size_t(256) << 20;
-constexpr int kGradScale = 15;        // G is stored times 2^15
+constexpr int kGradScale = kTcGradScale;   // G is stored times 2^15
 
 // ------------------------------------------------------------ packed -> fp16
 struct DequantParams {
@@ -150,24 +150,37 @@ struct LowrankParams {
   const int8_t* B;
   const uint16_t* s_B;
   uint16_t* out;
+  uint32_t* header;           // 64 words of the workspace: status, tickets
   int32_t d, rcp, rrp, Kz, g_B;
   float mul_c, mul_r;
 };
+// A thread per 8 columns; the first block also clears the workspace header.
 __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p) {
-  const int e = blockIdx.x;
+  if (blockIdx.x == 0 && threadIdx.x < 64) p.header[threadIdx.x] = 0u;
+  const int per = p.d / 8, i = blockIdx.x * 256 + threadIdx.x;
+  const int e = i / per, j = (i - e * per) * 8;
+  if (e >= p.Kz) return;
   const int k = (e & ~15) + tc_kcol(e & 15);
-  uint16_t* out = p.out + static_cast<size_t>(e) * p.d;
-  for (int j = threadIdx.x; j < p.d; j += blockDim.x) {
-    float v = 0.f;
-    if (k < p.rcp) {
-      v = static_cast<float>(p.R[static_cast<size_t>(k) * p.d + j]) * __half2float(__ushort_as_half(p.s_R[k])) * p.mul_c;
-    } else if (k - p.rcp < p.rrp) {
-      const int r = k - p.rcp;
-      v = static_cast<float>(p.B[static_cast<size_t>(r) * p.d + j]) *
-          __half2float(__ushort_as_half(p.s_B[static_cast<size_t>(r) * (p.d / p.g_B) + j / p.g_B])) * p.mul_r;
+  const bool core = k < p.rcp;
+  uint32_t o[4] = {0u, 0u, 0u, 0u};
+  if (core || k - p.rcp < p.rrp) {
+    const int r = core ? k : k - p.rcp;
+    const uint2 codes = __ldg(reinterpret_cast<const uint2*>((core ? p.R : p.B) + static_cast<size_t>(r) * p.d + j));
+    const int8_t* c8 = reinterpret_cast<const int8_t*>(&codes);
+    const uint16_t* sb = core ? nullptr : p.s_B + static_cast<size_t>(r) * (p.d / p.g_B);
+    const float mul = core ? __half2float(__ushort_as_half(p.s_R[r])) * p.mul_c : p.mul_r;
+#pragma unroll
+    for (int c = 0; c < 8; c += 2) {
+      float v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        v[h] = static_cast<float>(c8[c + h]) * mul;
+        if (!core) v[h] *= __half2float(__ushort_as_half(sb[(j + c + h) / p.g_B]));
+      }
+      o[c / 2] = pack_half2(v[0], v[1]);
     }
-    out[j] = __half_as_ushort(__float2half_rn(v));
   }
+  *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(e) * p.d + j) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // X of heads whose z the activation kernel does not compute (g_B not a multiple
@@ -253,6 +266,8 @@ struct DxParams {
 };
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   __shared__ float part[8];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int q0 = blockIdx.y * blockDim.x + threadIdx.x, dq = gridDim.y * blockDim.x;
   if (p.grad[t] == 0.f) {     // its row of dX is zero, S has no meaning
@@ -296,6 +311,25 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
           make_uint2(pack_half2(v.x * kInv, v.y * kInv), pack_half2(v.z * kInv, v.w * kInv));
     }
   }
+}
+
+// Launch as a programmatic dependent of the stream's previous kernel: the new
+// grid's blocks may be set up while it drains, and each waits for its end
+// (griddepcontrol.wait) before it touches memory that others write or read.
+template <class... Params, class... Args>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // -------------------------------------------------------------------- gemm
@@ -502,11 +536,6 @@ __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tme
   }
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ float grad_nan() { return __int_as_float(0x7fc00000); }
 
 // Columns in pieces of 32.  A lane holds one token's row of the accumulator; G
@@ -691,6 +720,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGWarps * 32, 1)
   cluster_sync();   // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *sm.tmem;
+  grid_dependency_wait();
+  grid_launch_dependents();
   if (warp == 0) g_tma_warp<kMode>(p, sm, &ma, &mb, pair, pairs, rank);
   else if (warp == 1) {
     if (rank == 0) g_mma_warp<kMode>(p, sm, tmem_base, pair, pairs);
@@ -720,8 +751,7 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
     p.half0 = 0;
     p.half_pairs = grid;
   }
-  grad_gemm_kernel<kMode><<<2 * grid, kGWarps * 32, kGSmem, stream>>>(p, ma, mb);
-  return cudaGetLastError();
+  return launch_after(grad_gemm_kernel<kMode>, dim3(2 * grid), kGWarps * 32, kGSmem, stream, p, ma, mb);
 }
 
 // ------------------------------------------------------- few tokens: G, G W~
@@ -743,6 +773,8 @@ struct GParams {
 constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
 __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
   __shared__ __align__(16) uint16_t piece[kGwRows / 8][32][8];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = blockIdx.x * kGwRows;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -928,6 +960,8 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem;
+  grid_dependency_wait();
+  grid_launch_dependents();
 
   // This CTA: column group, its chunks and blocks, its k-steps.
   // (Every groups-th block of 128 columns: the core and correction blocks at the
@@ -1250,7 +1284,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.fwd = ws_layout(h, T).total;
     at = round_up(o.fwd, 256);
     o.n_ssum = (L.n_mtiles + kGwMt - 1) / kGwMt;
-    o.logits = take(t * L.V * 4);
+    if (!use_tc(h, T)) o.logits = take(t * L.V * 4);
     const GwPlan g = gw_plan(h);
     o.splits = std::max(g.s_big, g.s_small);
   } else {
@@ -1264,7 +1298,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.xop = take(t * Kc * 2);
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
   }
-  o.ssum = take(o.n_ssum * t * 4);
+  o.ssum = take((o.few ? 4 : 1) * o.n_ssum * t * 4);
   o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
@@ -1356,30 +1390,33 @@ struct GradCall {
   int sigma;                  // dz carries 2^beta (2^gamma), the rows of R (B) 2^rho: both meet in 2^sigma
 };
 
-// The rows of R and B for the last product.
+// The rows of R and B for the last product; the header cleared (status word,
+// tickets of the activation kernel).
 int grad_lowrank(const GradCall& c) {
   const Layout& L = c.h.L;
-  if (c.o.Kz == 0) return ARCHEAD_OK;
+  if (c.o.Kz == 0) {
+    const cudaError_t e = cudaMemsetAsync(c.wb, 0, 256, c.stream);
+    return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
+  }
   LowrankParams lp{reinterpret_cast<const int8_t*>(c.h.arena + L.off_R),
                    reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sR),
                    reinterpret_cast<const int8_t*>(c.h.arena + L.off_B),
                    reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sB),
-                   reinterpret_cast<uint16_t*>(c.wb + c.o.rb), L.d, L.rcp, L.rrp, c.o.Kz, L.g_B,
+                   reinterpret_cast<uint16_t*>(c.wb + c.o.rb), reinterpret_cast<uint32_t*>(c.wb), L.d, L.rcp, L.rrp, c.o.Kz, L.g_B,
                    std::ldexp(1.f, c.sigma - c.h.tc_beta), std::ldexp(1.f, c.sigma - c.h.tc_gamma)};
-  lowrank_rows_kernel<<<c.o.Kz, 256, 0, c.stream>>>(lp);
+  lowrank_rows_kernel<<<(c.o.Kz * (L.d / 8) + 255) / 256, 256, 0, c.stream>>>(lp);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
 }
 
 // dX -> dh of one pass's tokens.
-int grad_finish(const GradCall& c, GemmParams& p, int splits, int splits_small, int groups, int big) {
+int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, int splits_small, int groups, int big) {
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
-  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, c.o.n_ssum, nt, Kc, L.d,
+  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, nt, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, splits_small, groups, big};
-  dx_kernel<<<dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream>>>(dp);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(dx_kernel, dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream, dp);
   CUtensorMap mz{}, mr{};
   if (e == cudaSuccess && Kz > 0) {
     e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM / 2);
@@ -1400,17 +1437,24 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   const archead_handle& h = c.h;
   const Layout& L = h.L;
   const int T = p.M;
-  float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
-  const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
-  if (rc != ARCHEAD_OK) return rc;
-  GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0};
-  g_kernel<<<dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream>>>(gp);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return set_cuda_error(e);
+  int n_ssum = c.o.n_ssum;
+  cudaError_t e;
+  if (use_tc(h, T)) {
+    n_ssum *= 4;
+    const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, c.wb, c.stream);
+    if (rc != ARCHEAD_OK) return rc;
+  } else {
+    float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
+    const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
+    if (rc != ARCHEAD_OK) return rc;
+    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0};
+    e = launch_after(g_kernel, dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream, gp);
+    if (e != cudaSuccess) return set_cuda_error(e);
+  }
   const GwPlan g = gw_plan(h);
   GwParams w{};
   w.rows = dequant_params(h, nullptr);
-  w.G = gp.G;
+  w.G = reinterpret_cast<const uint4*>(p.G);
   w.T = T;
   w.n_mtiles = L.n_mtiles;
   w.nk = g.nk;
@@ -1423,13 +1467,10 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   w.split_stride = p.split_stride;
   w.status = p.status;
   const int grid = g.big * g.s_big + (g.groups - g.big) * g.s_small;
-  if (w.rows.g_log2 >= 7) gw_kernel<1><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
-  else if (w.rows.g_log2 == 6) gw_kernel<2><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
-  else if (w.rows.g_log2 == 5) gw_kernel<4><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
-  else gw_kernel<8><<<grid, kGwWarps * 32, kGwSmem, c.stream>>>(w);
-  e = cudaGetLastError();
+  const auto kernel = w.rows.g_log2 >= 7 ? gw_kernel<1> : w.rows.g_log2 == 6 ? gw_kernel<2> : w.rows.g_log2 == 5 ? gw_kernel<4> : gw_kernel<8>;
+  e = launch_after(kernel, dim3(grid), kGwWarps * 32, kGwSmem, c.stream, w);
   if (e != cudaSuccess) return set_cuda_error(e);
-  return grad_finish(c, p, g.s_big, g.s_small, g.groups, g.big);
+  return grad_finish(c, p, n_ssum, g.s_big, g.s_small, g.groups, g.big);
 }
 
 // Many tokens: chunk by chunk through the dequantised rows.
@@ -1470,7 +1511,7 @@ int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
     e = launch_gemm<kAccumulate>(p, mg, mwn, h.num_sms, c.stream);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
-  return grad_finish(c, p, o.splits, o.splits, 1, 1);
+  return grad_finish(c, p, o.n_ssum, o.splits, o.splits, 1, 1);
 }
 
 int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T, const int32_t* targets,
@@ -1479,9 +1520,6 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
   GradCall c{h, o, wb, stream, L.r_c > 0 ? h.tc_beta + h.tc_rho_c : 1 << 20};
   if (L.r_r > 0) c.sigma = std::min(c.sigma, h.tc_gamma + h.tc_rho_r);
   if (o.Kz == 0) c.sigma = 0;
-  // The header: status word, tickets of the activation kernel.
-  const cudaError_t e = cudaMemsetAsync(wb, 0, 256, stream);
-  if (e != cudaSuccess) return set_cuda_error(e);
   int rc = grad_lowrank(c);
   for (int t0 = 0; t0 < T && rc == ARCHEAD_OK; t0 += o.tokens) {
     const int nt = std::min(o.tokens, T - t0);

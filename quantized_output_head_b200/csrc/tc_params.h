@@ -29,6 +29,8 @@ constexpr int kActPartFloats = 16 * 64 + 16;   // one split's partial sums and t
 constexpr int kActTicketOff = 64;     // workspace byte offset of the K-split tickets (inside the zeroed head)
 constexpr int kActTickets = 48;       // tickets available there: K splits need tiles x z blocks <= this
 
+constexpr int kTcGradScale = 15;      // the gradient's G is stored times 2^15: full precision down to 2^-29
+
 struct TcParams {
   const uint8_t* mtiles;      // arena: m-tile blocks
   const int32_t* targets;     // [T] or null
@@ -47,6 +49,11 @@ struct TcParams {
   int32_t stages, ring;                        // stage buffers (even, <= kTcMaxStages); ring slots per warp
   uint32_t acc_stride, acol0;                  // TMEM columns: accumulator stride, first A stage
   uint32_t bstage_bytes, ring_off, epi_off, bar_off;   // shared-memory plan
+  // gradient instance: G in place of the statistics (grad.cu)
+  const float* lse;           // [T]
+  const float* grad;          // [T]
+  uint4* G;                   // [128-row tile][ceil(T / 32)][16 runs of 8 rows][32 tokens]
+  float* ssum;                // [128-row tile][4][T]: sums of exp(y - lse) over 32 rows
 };
 
 struct ActParams {

@@ -531,6 +531,10 @@ __device__ void mma_warp(const TcParams& p, const TcSmem& sm, uint32_t tmem_base
 // target logit if it falls in these rows, and the logits row segment if asked.
 // The four warps' states of a token are merged into one partial per
 // (token, 128-row tile).
+// kGrad: what goes out is the gradient's G = exp(y - lse) - [row = target], fp16
+// times 2^kTcGradScale, a lane's token and 8 rows in one 16-byte run (the runs of
+// 32 tokens side by side), and the sum of exp(y - lse) over the 32 rows.
+template <bool kGrad>
 __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tmem_base, int ew, int lane) {
   grid_dependency_wait();   // 2^-c_t, and the previous call's readers of the outputs
   const int q = (kTcDeqWarps + 2 + ew) & 3;   // TMEM lane quarter of this warp
@@ -557,7 +561,34 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
         for (int jj = 0; jj < 32; ++jj) tile[jj * 33 + lane] = __uint_as_float(r[jj]);
         __syncwarp();
         const int col = c0 + lane;
-        if (col < ncol && nrow > 0) {
+        if constexpr (kGrad) {
+          // (one token tile: tb = 0; tokens past the last one get zeros)
+          const float g = col < ncol ? __ldg(p.grad + col) : 0.f;
+          const bool live = g != 0.f;   // its lse and target may be anything otherwise
+          const float k2 = live ? __ldg(p.cinv + col) * 1.44269504f : 0.f;
+          const float l2 = live ? __ldg(p.lse + col) * 1.44269504f - static_cast<float>(kTcGradScale) : 0.f;
+          const int tg = live ? __ldg(p.targets + col) - p.row0 - v0 : -1;   // row within this warp's 32
+          float y[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[k] = exp2_approx(fmaf(tile[lane * 33 + k], k2, -l2));
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            if (!live || k >= nrow) y[k] = 0.f;
+            sum += y[k];
+          }
+          if (__any_sync(0xffffffffu, tg >= 0 && tg < nrow)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (k == tg && k < nrow) y[k] -= static_cast<float>(1 << kTcGradScale);
+          }
+          uint4* dst = p.G + (static_cast<size_t>(mt) * ((p.T + 31) / 32) + c0 / 32) * (kTcBM / 8 * 32) + 4 * q * 32 + lane;
+#pragma unroll
+          for (int r8 = 0; r8 < 4; ++r8)
+            dst[32 * r8] = make_uint4(pack_half2(y[8 * r8], y[8 * r8 + 1]), pack_half2(y[8 * r8 + 2], y[8 * r8 + 3]),
+                                      pack_half2(y[8 * r8 + 4], y[8 * r8 + 5]), pack_half2(y[8 * r8 + 6], y[8 * r8 + 7]));
+          if (col < ncol) p.ssum[(static_cast<size_t>(mt) * 4 + q) * p.T + col] = sum * (1.f / (1 << kTcGradScale));
+        } else if (col < ncol && nrow > 0) {
           const int t = tb + col;
           const float inv = __ldg(p.cinv + t);
           float y[32];
@@ -596,6 +627,7 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&sm.acce[a]));
+    if constexpr (kGrad) continue;
     // The four warps' states of each token -> one partial per (token, tile).
     named_bar_sync(1, 128);
     const int col = ew * 32 + lane;
@@ -617,7 +649,7 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
 
 // 22 warps: an SM sub-partition holds up to six of them, and its 16,384
 // registers allow 80 per thread.
-template <int R>
+template <int R, bool kGrad>
 __global__ void __launch_bounds__(kTcWarps * 32, 1)
     tc_kernel(const TcParams p, const __grid_constant__ CUtensorMap xmap) {
   extern __shared__ uint8_t smem_raw[];
@@ -648,7 +680,7 @@ __global__ void __launch_bounds__(kTcWarps * 32, 1)
   if (warp < kTcDeqWarps) dequant_warp<R>(p, sm, tmem_base, warp, lane);
   else if (warp == kTcDeqWarps) tma_warp(p, sm, &xmap, lane);
   else if (warp == kTcDeqWarps + 1) mma_warp(p, sm, tmem_base, lane);
-  else epilogue_warps(p, sm, tmem_base, warp - kTcDeqWarps - 2, lane);
+  else epilogue_warps<kGrad>(p, sm, tmem_base, warp - kTcDeqWarps - 2, lane);
 
   tc_fence_before();
   __syncthreads();
@@ -743,12 +775,13 @@ size_t tc_smem_max() {
 }
 
 namespace {
+template <bool kGrad>
 const void* tc_kernel_for(int ring) {
   switch (ring) {
-    case 2: return reinterpret_cast<const void*>(&tc_kernel<2>);
-    case 3: return reinterpret_cast<const void*>(&tc_kernel<3>);
-    case 4: return reinterpret_cast<const void*>(&tc_kernel<4>);
-    default: return reinterpret_cast<const void*>(&tc_kernel<5>);
+    case 2: return reinterpret_cast<const void*>(&tc_kernel<2, kGrad>);
+    case 3: return reinterpret_cast<const void*>(&tc_kernel<3, kGrad>);
+    case 4: return reinterpret_cast<const void*>(&tc_kernel<4, kGrad>);
+    default: return reinterpret_cast<const void*>(&tc_kernel<5, kGrad>);
   }
 }
 }  // namespace
@@ -757,7 +790,9 @@ cudaError_t tc_set_attributes() {
   const int smem = static_cast<int>(tc_smem_max());
   cudaError_t e = cudaSuccess;
   for (int r = kTcMinRing; r <= kTcMaxRing && e == cudaSuccess; ++r)
-    e = cudaFuncSetAttribute(tc_kernel_for(r), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(tc_kernel_for<false>(r), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  for (int r = kTcMinRing; r <= kTcMaxRing && e == cudaSuccess; ++r)
+    e = cudaFuncSetAttribute(tc_kernel_for<true>(r), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
 }
 
@@ -809,7 +844,7 @@ cudaError_t launch_tc(const TcParams& p, const CUtensorMap& map, int grid, cudaS
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   void* args[] = {const_cast<TcParams*>(&p), const_cast<CUtensorMap*>(&map)};
-  return cudaLaunchKernelExC(&cfg, tc_kernel_for(p.ring), args);
+  return cudaLaunchKernelExC(&cfg, p.G != nullptr ? tc_kernel_for<true>(p.ring) : tc_kernel_for<false>(p.ring), args);
 }
 
 cudaError_t launch_tc_merge(const float4* partials, int n_mt128, int T, const int32_t* targets, const float* tgt,
