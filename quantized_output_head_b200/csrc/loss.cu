@@ -56,14 +56,15 @@ struct TokenArgs {
   const float* ce_ref;        // or null
   const uint8_t* mask;        // or null
   const int32_t* cu;          // [S + 1], or null: one sequence of T tokens
-  int32_t T, S, unit;         // unit: tokens per warp, a multiple of kGroup
+  int32_t T, S, unit;         // unit: tokens per warp, 32, 64 or a multiple of kGroup
   int32_t vec;                // every token array is 16-byte (mask: 4-byte) aligned
   float* grad;
   double* seg_sum;            // [S] sum of a sequence's first piece
   double* open_sum;           // [units] sum of the piece a unit begins with
   int32_t* seg_n;             // the same for counted tokens
   int32_t* open_n;
-  float* coef;                // [S] per-sequence factor
+  float* coef;                // [S] gradient of a sequence's tokens (preference loss)
+  double* each;               // [S] 1 / counted tokens (policy loss)
   double* part;               // [blocks][4] sums of a block
   int32_t* part_n;            // [blocks][2]
 };
@@ -194,57 +195,128 @@ __device__ __forceinline__ double exp_k3(double x, double& k3) {
 }
 
 // Sums and counts of the pieces of sequences in this warp's run of tokens.
-// kSum: also the sum of (ce_ref - ce).
+// kSum: also the sum of (ce_ref - ce).  A group inside one sequence adds to
+// per-lane sums; one with boundaries goes 32 tokens at a time through a
+// segmented scan (the same steps however many sequences begin in it).
 template <bool kSum>
 __device__ void walk_segments(const TokenArgs& a, int unit, int lane) {
   const int u0 = unit * a.unit, u1 = min(u0 + a.unit, a.T);
   if (u0 >= u1) return;
-  int s = seq_of_warp(a, u0, lane);
-  if (s < 0) s = 0;   // the run begins before the first sequence
+  int s = seq_of_warp(a, u0, lane);   // -1: before the first sequence, S: after the last
+  int cs = 0, ce = 0;                 // of s, where it is one
   double sum = 0.0;
-  int n = 0;
-  int cs = s < a.S ? cu_at(a, s) : a.T, ce = s < a.S ? cu_at(a, s + 1) : a.T;
-  auto flush = [&]() {
-    if constexpr (kSum) sum = warp_sum(sum);
-    n = warp_sum(n);
-    if (lane == 0) {
-      if (cs >= u0) {
-        if constexpr (kSum) a.seg_sum[s] = sum;
-        a.seg_n[s] = n;
-      } else {
-        if constexpr (kSum) a.open_sum[unit] = sum;
-        a.open_n[unit] = n;
-      }
+  int n = 0;                          // of s so far, per lane
+  auto enter = [&]() {
+    if (s >= 0 && s < a.S) {
+      cs = cu_at(a, s);
+      ce = cu_at(a, s + 1);
     }
-    sum = 0.0;
-    n = 0;
   };
-  for (int g = u0; g < u1 && s < a.S; g += kGroup) {
-    const int t = g + 4 * lane, g1 = min(g + kGroup, u1);
-    const uint32_t keep = keep4(a, t);
-    float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (kSum) {
-      load4(a.ce, t, a.T, a.vec, x);
-      if (a.ce_ref != nullptr) load4(a.ce_ref, t, a.T, a.vec, y);
+  auto put = [&](int seq, int begin, double v, int c) {
+    if (begin >= u0) {
+      if constexpr (kSum) a.seg_sum[seq] = v;
+      a.seg_n[seq] = c;
+    } else {
+      if constexpr (kSum) a.open_sum[unit] = v;
+      a.open_n[unit] = c;
     }
-    for (;;) {
-      const int b = max(cs, g), e = min(ce, g1);
+  };
+  enter();
+  for (int g = u0; g < u1; g += kGroup) {
+    const int t = g + 4 * lane, g1 = min(g + kGroup, u1);
+    if (s >= 0 && s < a.S && cs <= g && ce >= g1) {
+      const uint32_t keep = keep4(a, t);
+      float x[4], y[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (kSum) {
+        load4(a.ce, t, a.T, a.vec, x);
+        if (a.ce_ref != nullptr) load4(a.ce_ref, t, a.T, a.vec, y);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (t + i >= b && t + i < e && (keep >> i & 1u)) {
+        if (t + i < g1 && (keep >> i & 1u)) {
           if constexpr (kSum) sum += static_cast<double>(y[i]) - static_cast<double>(x[i]);
           ++n;
         }
       }
-      if (ce > g1) break;          // goes on in the next group (or the next run)
-      if (ce > cs) flush();
-      if (++s >= a.S) break;
-      cs = ce;
-      ce = cu_at(a, s + 1);
-      if (cs >= g1) break;
+      if (ce > g1) continue;   // (the common case: goes on in the next group or run)
+      if constexpr (kSum) sum = warp_sum(sum);
+      n = warp_sum(n);
+      if (lane == 0) put(s, cs, sum, n);
+      sum = 0.0;
+      n = 0;
+      s = seq_from(a, g1, s);
+      enter();
+      continue;
     }
+    // What s has so far, in every lane.
+    double run = kSum ? warp_sum(sum) : 0.0;
+    int run_n = warp_sum(n), run_s = s;
+    double val[4];
+    bool cnt[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {   // all loads of the group first
+      const int tt = g + 32 * i + lane;
+      cnt[i] = tt < g1 && (a.mask == nullptr || a.mask[tt] != 0);
+      val[i] = 0.0;
+      if constexpr (kSum)
+        if (tt < g1) val[i] = (a.ce_ref != nullptr ? static_cast<double>(a.ce_ref[tt]) : 0.0) - static_cast<double>(a.ce[tt]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int h = g + 32 * i, tt = h + lane;
+      if (h >= g1) break;
+      int q = -1, qs = 0, qe = 0;
+      if (tt < g1) {
+        q = seq_from(a, tt, run_s);
+        if (q >= a.S) q = -1;
+        if (q >= 0) {
+          qs = cu_at(a, q);
+          qe = cu_at(a, q + 1);
+          if (tt >= qe) q = -1;
+        }
+      }
+      const bool counts = q >= 0 && cnt[i];
+      double v = counts ? val[i] : 0.0;
+      int c = counts ? 1 : 0;
+      const int before = __shfl_up_sync(0xffffffffu, q, 1), after = __shfl_down_sync(0xffffffffu, q, 1);
+      bool head = lane == 0 || q != before;
+      const bool tail = lane == 31 || q != after;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int cc = __shfl_up_sync(0xffffffffu, c, o);
+        const bool hh = __shfl_up_sync(0xffffffffu, head ? 1 : 0, o) != 0;
+        double vv = 0.0;
+        if constexpr (kSum) vv = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o && !head) {
+          if constexpr (kSum) v += vv;
+          c += cc;
+          head = hh;
+        }
+      }
+      if (q >= 0 && q == run_s) {   // begun before these 32
+        if constexpr (kSum) v += run;
+        c += run_n;
+      }
+      const bool ends = q >= 0 && tt + 1 >= qe;
+      if (tail && ends) put(q, qs, v, c);
+      // the sequence of the last token goes on, or nothing does
+      const int last = min(31, g1 - 1 - h);
+      const bool on = __shfl_sync(0xffffffffu, q >= 0 && !ends ? 1 : 0, last) != 0;
+      const int lq = __shfl_sync(0xffffffffu, q, last);
+      if constexpr (kSum) run = on ? __shfl_sync(0xffffffffu, v, last) : 0.0;
+      run_n = on ? __shfl_sync(0xffffffffu, c, last) : 0;
+      if (lq >= 0) run_s = lq;
+    }
+    s = seq_from(a, g1, run_s);
+    enter();
+    sum = lane == 0 ? run : 0.0;
+    n = lane == 0 ? run_n : 0;
   }
-  if (s < a.S && cs < u1 && ce > u1) flush();   // unfinished at the end of the run
+  if (s >= 0 && s < a.S && cs < u1 && ce > u1) {   // unfinished at the end of the run
+    if constexpr (kSum) sum = warp_sum(sum);
+    n = warp_sum(n);
+    if (lane == 0) put(s, cs, sum, n);
+  }
 }
 
 // Counted tokens (and the sum) of sequence s, from its pieces, by one warp.
@@ -255,6 +327,7 @@ __device__ __forceinline__ int sequence_total(const TokenArgs& a, int s, int lan
   if (ce <= cs) return 0;
   const int ua = cs / a.unit, ub = (ce - 1) / a.unit;
   int n = 0;
+#pragma unroll 4
   for (int u = ua + 1 + lane; u <= ub; u += 32) {
     if constexpr (kSum) sum += a.open_sum[u];
     n += a.open_n[u];
@@ -265,6 +338,41 @@ __device__ __forceinline__ int sequence_total(const TokenArgs& a, int s, int lan
   }
   if constexpr (kSum) sum = warp_sum(sum);
   return warp_sum(n);
+}
+
+// The same for a sequence per lane (-1: none): the lane adds the pieces of a
+// short one, the warp together those of a long one.
+template <bool kSum>
+__device__ __forceinline__ int lane_total(const TokenArgs& a, int s, int lane, double& sum) {
+  constexpr int kAlone = 8;
+  int n = 0, ua = 0, ub = -1;
+  sum = 0.0;
+  if (s >= 0) {
+    const int cs = cu_at(a, s), ce = cu_at(a, s + 1);
+    if (ce > cs) {
+      ua = cs / a.unit;
+      ub = (ce - 1) / a.unit;
+    }
+  }
+  const bool together = ub - ua > kAlone;
+  if (ub >= ua && !together) {
+    if constexpr (kSum) sum = a.seg_sum[s];
+    n = a.seg_n[s];
+    for (int u = ua + 1; u <= ub; ++u) {
+      if constexpr (kSum) sum += a.open_sum[u];
+      n += a.open_n[u];
+    }
+  }
+  for (uint32_t todo = __ballot_sync(0xffffffffu, together); todo != 0; todo &= todo - 1) {
+    const int who = __ffs(todo) - 1;
+    double v;
+    const int c = sequence_total<kSum>(a, __shfl_sync(0xffffffffu, s, who), lane, v);
+    if (lane == who) {
+      sum = v;
+      n = c;
+    }
+  }
+  return n;
 }
 
 // Walks a run in groups and hands each lane's four tokens their sequence (-1:
@@ -278,21 +386,22 @@ __device__ __forceinline__ void for_tokens(const TokenArgs& a, int unit, int lan
     const int t = g + 4 * lane;
     int q[4];
     const int next = s < a.S ? cu_at(a, s + 1) : a.T + 1;   // (s = -1: the first sequence's begin)
-    if (next >= min(g + kGroup, u1)) {
+    const int g1 = min(g + kGroup, u1);
+    if (next >= g1) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = s >= 0 && s < a.S ? s : -1;
     } else {
       int from = s;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int z = seq_from(a, min(t + i, a.T - 1), from);
+        int z = seq_from(a, min(t + i, g1 - 1), from);
         from = z;
         if (z >= a.S || (z >= 0 && t + i >= cu_at(a, z + 1))) z = -1;
         q[i] = z;
       }
       s = __shfl_sync(0xffffffffu, from, 31);
     }
-    body(t, q);
+    if (t < g1) body(t, q);   // (a run is a multiple of four tokens)
   }
 }
 
@@ -345,13 +454,19 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
   }
   int total = 0, alive = 0;
   if (by_sequence) {
-    for (int s = unit; s < a.S; s += units) {
+    const int each = min(32, (a.S + units - 1) / units);   // sequences of a warp at a time
+    for (int s0 = each * unit; s0 < a.S; s0 += each * units) {
+      const int s = lane < each && s0 + lane < a.S ? s0 + lane : -1;
       double unused;
-      const int n = a.mask != nullptr ? sequence_total<false>(a, s, lane, unused) : max(0, cu_at(a, s + 1) - cu_at(a, s));
-      if (lane == 0) a.coef[s] = n > 0 ? 1.f / static_cast<float>(n) : 0.f;
+      int n = 0;
+      if (a.mask != nullptr) n = lane_total<false>(a, s, lane, unused);
+      else if (s >= 0) n = max(0, cu_at(a, s + 1) - cu_at(a, s));
+      if (s >= 0) a.each[s] = n > 0 ? 1.0 / n : 0.0;
       total += n;
       alive += n > 0 ? 1 : 0;
     }
+    total = warp_sum(total);
+    alive = warp_sum(alive);
   } else if (a.mask != nullptr) {
     const int b = max(unit * a.unit, cu_at(a, 0)), e = min(min((unit + 1) * a.unit, a.T), cu_at(a, a.S));
     for (int t = unit * a.unit + 4 * lane; t < e; t += kGroup) {
@@ -395,7 +510,7 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
       g[i] = 0.f;
       if (q[i] < 0 || !(keep >> i & 1u)) continue;
       const double adv = p.per_sequence ? __ldg(p.adv + q[i]) : A[i];
-      const double w = by_sequence ? all * a.coef[q[i]] : all;
+      const double w = by_sequence ? all * a.each[q[i]] : all;
       const double D = static_cast<double>(o[i]) - static_cast<double>(x[i]);
       double k3;
       const double ratio = exp_k3(D, k3);
@@ -437,9 +552,12 @@ __global__ void __launch_bounds__(kLossThreads, 1) preference_loss_kernel(const 
   walk_segments<true>(a, unit, lane);
   meet<kMeet>();
   double loss = 0.0;
-  for (int i = unit; i < p.N; i += units) {
+  const int each = min(32, (p.N + units - 1) / units);   // pairs of a warp at a time
+  for (int i0 = each * unit; i0 < p.N; i0 += each * units) {
+    const int i = lane < each && i0 + lane < p.N ? i0 + lane : -1;
     double sc, sr;
-    const int nc = sequence_total<true>(a, i, lane, sc), nr = sequence_total<true>(a, p.N + i, lane, sr);
+    const int nc = lane_total<true>(a, i, lane, sc), nr = lane_total<true>(a, i < 0 ? -1 : p.N + i, lane, sr);
+    if (i < 0) continue;
     const double fc = p.average ? 1.0 / max(nc, 1) : 1.0, fr = p.average ? 1.0 / max(nr, 1) : 1.0;
     sc *= fc;
     sr *= fr;
@@ -462,15 +580,13 @@ __global__ void __launch_bounds__(kLossThreads, 1) preference_loss_kernel(const 
         slope = p.beta * (p.smooth * s_pos - (1.0 - p.smooth) * s_neg);
       }
     }
-    if (lane == 0) {
-      const double f = p.scale / p.N;
-      a.coef[i] = static_cast<float>(-slope * fc * f);
-      a.coef[p.N + i] = static_cast<float>(slope * fr * f);
-      p.rewards[i] = static_cast<float>(p.beta * sc);
-      p.rewards[p.N + i] = static_cast<float>(p.beta * sr);
-    }
+    const double f = p.scale / p.N;
+    a.coef[i] = static_cast<float>(-slope * fc * f);
+    a.coef[p.N + i] = static_cast<float>(slope * fr * f);
+    p.rewards[i] = static_cast<float>(p.beta * sc);
+    p.rewards[p.N + i] = static_cast<float>(p.beta * sr);
   }
-  block_sums<1>(a, {loss}, warp, lane);
+  block_sums<1>(a, {warp_sum(loss)}, warp, lane);
   meet<kMeet>();
   for_tokens(a, unit, lane, [&](int t, const int (&q)[4]) {
     if (t >= a.T) return;
@@ -494,7 +610,7 @@ bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p)
 
 // Workspace: pieces per sequence and per unit, factors per sequence.
 struct LossLayout {
-  size_t seg_sum, open_sum, seg_n, open_n, coef, part, part_n, total;
+  size_t seg_sum, open_sum, seg_n, open_n, coef, each, part, part_n, total;
 };
 LossLayout loss_layout(int S) {
   LossLayout o{};
@@ -510,6 +626,7 @@ LossLayout loss_layout(int S) {
   o.seg_n = take(s * 4);
   o.open_n = take(kMaxUnits * 4);
   o.coef = take(s * 4);
+  o.each = take(s * 8);
   o.part = take(kLossMaxBlocks * 32);
   o.part_n = take(kLossMaxBlocks * 8);
   o.total = at;
@@ -544,8 +661,9 @@ void token_args(TokenArgs& a, const float* ce, const float* ce_ref, const uint8_
   a.cu = cu;
   a.T = T;
   a.S = S;
-  a.unit = static_cast<int>(round_up((T + blocks * kLossWarps - 1) / (blocks * kLossWarps), kGroup));
-  if (a.unit == 0) a.unit = kGroup;
+  // whole groups, or a part of one so that few tokens still spread over the warps
+  const int per = (T + blocks * kLossWarps - 1) / (blocks * kLossWarps);
+  a.unit = per <= 32 ? 32 : per <= 64 ? 64 : static_cast<int>(round_up(per, kGroup));
   a.vec = aligned(ce, 16) && aligned(ce_ref, 16) && aligned(mask, 4) && aligned(grad, 16) ? 1 : 0;
   a.grad = grad;
   a.seg_sum = reinterpret_cast<double*>(w + o.seg_sum);
@@ -553,6 +671,7 @@ void token_args(TokenArgs& a, const float* ce, const float* ce_ref, const uint8_
   a.seg_n = reinterpret_cast<int32_t*>(w + o.seg_n);
   a.open_n = reinterpret_cast<int32_t*>(w + o.open_n);
   a.coef = reinterpret_cast<float*>(w + o.coef);
+  a.each = reinterpret_cast<double*>(w + o.each);
   a.part = reinterpret_cast<double*>(w + o.part);
   a.part_n = reinterpret_cast<int32_t*>(w + o.part_n);
 }
