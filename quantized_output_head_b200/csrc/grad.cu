@@ -249,6 +249,16 @@ __device__ __forceinline__ float4 packed_row4(const DequantParams& p, const uint
   return make_float4(lo.x * s, lo.y * s, hi.x * s, hi.y * s);
 }
 
+constexpr int kGwCols = 256, kGwChunks = kGwCols / 64;   // column block of gw_kernel
+// Row splits of the column blocks: the first `res` blocks are residual alone,
+// then come `rest` with core, correction or mixed chunks (the last may be short).
+struct GwSplits {
+  int32_t res, rest, s_res, s_rest, s_last;
+};
+__host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) {
+  return block < g.res ? g.s_res : block + 1 < g.res + g.rest ? g.s_rest : g.s_last;
+}
+
 // Blocks of 1024 columns per token: S from the tiles' partial sums (in a fixed order), then
 // dX (added over the K splits) / S + (1/S - 1) W~[target]; the residual columns
 // stay fp32 in the first split's place, the low-rank ones become the fp16
@@ -262,7 +272,8 @@ struct DxParams {
   size_t split_stride;
   uint16_t* dz;
   int32_t n_ssum, tokens, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
-  int32_t splits, splits_small, groups, big;       // partial dX of a block of 128 columns b: `splits` if b % groups < big
+  int32_t splits;                                  // partial dX of every column, or (0) by
+  GwSplits gw;
 };
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   __shared__ float part[8];
@@ -295,7 +306,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   float* dx = p.dx + static_cast<size_t>(t) * p.Kc;
   for (int q = q0; q < p.Kc / 4; q += dq) {
     float4 v = reinterpret_cast<const float4*>(dx)[q];
-    const int n = (q / 32) % p.groups < p.big ? p.splits : p.splits_small;
+    const int n = p.splits > 0 ? p.splits : gw_splits(p.gw, 4 * q / kGwCols);
     for (int s = 1; s < n; ++s) {
       const float4 x = reinterpret_cast<const float4*>(dx + s * p.split_stride)[q];
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
@@ -802,29 +813,29 @@ __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
 }
 
 // dX = G W~ for up to 128 tokens, the packed rows dequantised on the way:
-// D[128 tokens x 128 columns of W~] per accumulator, A = 128 columns of G in
-// TMEM, B = a 128-row x 128-column tile of W~ as the dequantising warps leave it
-// in shared memory (rows of 64 columns, so MN-major: the transpose costs
-// nothing).  The MMA reads its shared-memory operands at about 64 bytes a
-// clock, so with G there too a tile took nearly twice its clocks of math; and a
-// barrier round (wait, fence, commit) costs the MMA warp and the dequantising
-// warps some 250 clocks each whatever the tile, so tiles of 64 rows were bound
-// by that.  A CTA owns up to three column blocks (three accumulators and two
-// buffers of G fill the 512 TMEM columns) and a range of vocabulary rows, writes
-// one partial dX, and dx_kernel adds the partials of a column's CTAs in order.
-//   warps 0-15  dequantise: set w / 4 takes every fourth tile, a warp two 16-row
-//               m-tiles of it, their packed bytes loaded one of its tiles
-//               early straight into registers (one 16-byte load per lane and 64
+// D[128 tokens x 256 columns of W~] in TMEM, A = 128 columns of G in TMEM, B = a
+// 128-row x 256-column tile of W~ as the dequantising warps leave it in shared
+// memory (rows of 64 columns, so MN-major: the transpose costs nothing).  A CTA
+// owns one block of 256 columns and a range of vocabulary rows, writes one
+// partial dX, and dx_kernel adds the partials of a column's CTAs in order.
+//   warps 0-15  dequantise: set w / 8 takes every second tile, a warp one 16-row
+//               m-tile of it, its packed bytes loaded one of its tiles early
+//               straight into registers (one 16-byte load per lane and 64
 //               columns: nothing to copy, wait for or re-read).
 //   warps 16-19 G: the 32 tokens of their TMEM lane quarter, a k-step ahead in
 //               registers; warp 19 also issues the MMAs (as a duty of warps 0-15
 //               G cost the schedulers of the first quarters two thirds more
 //               instructions than the others).
-// Afterwards warps 0-15 write the accumulators.
-constexpr int kGwWarps = 20, kGwSets = 4, kGwStages = 4, kGwBlocks = 3, kGwBufs = 2;
+// Afterwards warps 0-15 write the accumulator.
+// What set the shape: the tensor cores read shared-memory operands at about 64
+// bytes a clock, so G sits in TMEM (with both operands in shared memory a tile
+// took nearly twice its clocks of math); a barrier round (wait, fence, commit)
+// and the issue of an MMA cost the MMA warp about 450 and 48 clocks, so a tile is
+// 8 MMAs of 256 columns (with 128 columns, 840 clocks a tile for 512 of math).
+constexpr int kGwWarps = 20, kGwSets = 2, kGwStages = 3, kGwBufs = 4;
 constexpr int kGwMma = kGwWarps - 1;                  // the warp that issues the MMAs
 constexpr uint32_t kGwHalf = kGwRows * 128;           // 128 rows x 64 columns of fp16
-constexpr uint32_t kGwTile = 2 * kGwHalf;
+constexpr uint32_t kGwTile = kGwChunks * kGwHalf;
 constexpr uint32_t kGwBarOff = kGwStages * kGwTile;
 constexpr uint32_t kGwSmem = kGwBarOff + 512 + 1024;
 
@@ -834,7 +845,7 @@ struct GwParams {
   int32_t T;
   int32_t n_mtiles, nk;        // k-steps of kGwRows rows
   int32_t chunks;              // 64-column chunks in all
-  int32_t groups, big, s_big, s_small;   // group g: column blocks g, g + groups, ...; row splits of the first `big`, the others
+  GwSplits splits;
   float* dx;                   // [split][T][Kc]
   size_t split_stride;
   uint32_t* status;
@@ -941,7 +952,7 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kGwStages; ++s) {
-      mbar_init(wfull + 8 * s, 4);
+      mbar_init(wfull + 8 * s, 8);
       mbar_init(wempty + 8 * s, 1);
     }
     for (int s = 0; s < kGwBufs; ++s) {
@@ -963,98 +974,74 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // This CTA: column group, its chunks and blocks, its k-steps.
-  // (Every groups-th block of 128 columns: the core and correction blocks at the
-  // end, which take longer to unpack, fall to different groups.)
-  const int u = blockIdx.x;
-  const bool in_big = u < p.big * p.s_big;
-  const int splits = in_big ? p.s_big : p.s_small, v = in_big ? u : u - p.big * p.s_big;
-  const int group = (in_big ? 0 : p.big) + v / splits, split = v % splits;
-  const int blocks = (p.chunks + 1) / 2, nbl = (blocks - group + p.groups - 1) / p.groups;
-  const int cstep = 2 * p.groups, c0 = 2 * group;   // chunk of block b: c0 + cstep b
+  // This CTA: column block, its chunks, its k-steps.
+  const GwSplits& g = p.splits;
+  int block, split = blockIdx.x;
+  if (split < g.res * g.s_res) {
+    block = split / g.s_res;
+    split -= block * g.s_res;
+  } else {
+    split -= g.res * g.s_res;
+    block = min(split / g.s_rest, g.rest - 1);
+    split -= block * g.s_rest;
+    block += g.res;
+  }
+  const int splits = gw_splits(g, block);
+  const int c0 = block * kGwChunks, nc = min(kGwChunks, p.chunks - c0);
   const int k0 = static_cast<int>(static_cast<int64_t>(p.nk) * split / splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(p.nk) * (split + 1) / splits);
-  const int steps = k1 - k0, total = steps * nbl;
+  const int steps = k1 - k0;
 
   if (warp < 16) {
-    const int set = warp >> 2, j = warp & 3;
+    const int set = warp >> 3, j = warp & 7;
     const int gr = lane >> 2, cc = lane & 3;
-    // byte offsets of this lane inside a tile: row 16 j + gr (and 64 below), 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
+    // byte offsets of this lane inside a tile: row 16 j + gr, 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
     const uint32_t row = tiles + static_cast<uint32_t>((16 * j + gr) * 128);
     const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16), o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
-    // the ring stage of this set's next tile
-    int s = set;
-    uint32_t ph = 1;
-    auto filled = [&]() {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(wfull + 8 * s);
-      s += kGwSets;
-      if (s >= kGwStages) {
-        s -= kGwStages;
-        ph ^= 1u;
-      }
-    };
 
-    // The next tile's packed bytes, both m-tiles.  Every load has its own
+    // The next tile's packed bytes, two pairs of chunks.  Every load has its own
     // register and at most a predicate: a load under a branch that others share a
     // register with would have to land before the branch ends.
-    RawPair<GP> raw[2];
     constexpr int kPer = RawPair<GP>::kPer;
-    int pk = k0, pb = set;
-    const uint8_t* pm = p.rows.mtiles + static_cast<size_t>(kGwMt * k0 + j) * p.rows.mblk_bytes;
-    const size_t next_k = static_cast<size_t>(kGwMt) * p.rows.mblk_bytes, half = static_cast<size_t>(4) * p.rows.mblk_bytes;
-    uint32_t code_off[2], scale_off[2], scale_step[2];   // of the block's chunks
-    bool core[2], corr2[2];
-    auto aim = [&]() {
-      while (pb >= nbl) {
-        pb -= nbl;
-        ++pk;
-        pm += next_k;
-      }
+    RawPair<GP> raw[2];
+    uint32_t code_off[kGwChunks], scale_off[kGwChunks];
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        const int ks = min(c0 + cstep * pb + ch, p.chunks - 1), kc = ks - p.rows.n_res, ka = 2 * (kc - p.rows.n_L);
-        const bool res = kc < 0;
-        core[ch] = !res && ka < 0;
-        corr2[ch] = ka >= 0 && ka + 1 < p.rows.n_A;
-        code_off[ch] = lane * 16 + (res ? p.rows.off_res + ks * kResChunkBytes
-                                        : ka < 0 ? p.rows.off_Lnib + kc * kLNibChunkBytes : p.rows.off_A + ka * kAChunkBytes);
-        scale_off[ch] = gr * 4 + (res ? p.rows.off_sres + ((ks * 64) >> p.rows.g_log2) * kSresGroupBytes
-                                      : ka < 0 ? p.rows.off_sL : p.rows.off_sA);
-        scale_step[ch] = res ? kSresGroupBytes : 0;
-      }
-    };
+    for (int ch = 0; ch < kGwChunks; ++ch) {
+      const int ks = min(c0 + ch, p.chunks - 1), kc = ks - p.rows.n_res, ka = 2 * (kc - p.rows.n_L);
+      code_off[ch] = lane * 16 + (kc < 0 ? p.rows.off_res + ks * kResChunkBytes
+                                         : ka < 0 ? p.rows.off_Lnib + kc * kLNibChunkBytes : p.rows.off_A + ka * kAChunkBytes);
+      scale_off[ch] = gr * 4 + (kc < 0 ? p.rows.off_sres + ((ks * 64) >> p.rows.g_log2) * kSresGroupBytes
+                                       : ka < 0 ? p.rows.off_sL : p.rows.off_sA);
+    }
+    int pk = k0 + set;
+    const uint8_t* pm = p.rows.mtiles + static_cast<size_t>(kGwMt * pk + j) * p.rows.mblk_bytes;
+    const size_t next_k = static_cast<size_t>(kGwSets * kGwMt) * p.rows.mblk_bytes;
     auto load = [&](RawPair<GP>& r, int i) {
-      // (past the end of the walk or of the rows: any valid bytes)
-      const bool in = pk < k1 && kGwMt * pk + j + 4 * i < p.n_mtiles;
-      const uint8_t* m = in ? pm + (i ? half : 0) : p.rows.mtiles;
+      // (past the end of the rows: any valid bytes)
+      const uint8_t* m = pk < k1 && kGwMt * pk + j < p.n_mtiles ? pm : p.rows.mtiles;
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
-        r.c[ch] = ldg128(m + code_off[ch]);
+        const int e = 2 * i + ch, ks = min(c0 + e, p.chunks - 1), kc = ks - p.rows.n_res, ka = 2 * (kc - p.rows.n_L);
+        r.c[ch] = ldg128(m + code_off[e]);
 #pragma unroll
-        for (int g = 0; g < kPer; ++g) r.s[ch * kPer + g] = ldg32(m + scale_off[ch] + g * scale_step[ch]);
-        if (core[ch]) r.x[ch].x = ldg32(m + p.rows.off_Lhi + (code_off[ch] - p.rows.off_Lnib) / 4);
-        if (corr2[ch]) r.x[ch] = ldg128(m + code_off[ch] + kAChunkBytes);
+        for (int q = 0; q < kPer; ++q) r.s[ch * kPer + q] = ldg32(m + scale_off[e] + (kc < 0 ? q * kSresGroupBytes : 0));
+        if (kc >= 0 && ka < 0) r.x[ch].x = ldg32(m + p.rows.off_Lhi + (code_off[e] - p.rows.off_Lnib) / 4);
+        if (ka >= 0 && ka + 1 < p.rows.n_A) r.x[ch] = ldg128(m + code_off[e] + kAChunkBytes);
       }
     };
-    aim();
     load(raw[0], 0);
     load(raw[1], 1);
-    int b = set, k = k0;
-    for (int it = set; it < total; it += kGwSets) {
-      while (b >= nbl) {
-        b -= nbl;
-        ++k;
-      }
+    int s = set;
+    uint32_t ph = 1;
+    for (int k = k0 + set; k < k1; k += kGwSets) {
       if (!warp_wait(flag, wempty + 8 * s, ph, p.status)) break;
-      const int c = c0 + cstep * b;
-      pb += kGwSets;
-      aim();
+      pk += kGwSets;
+      pm += next_k;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = o_lo + s * kGwTile + i * 64 * 128, hi = o_hi + s * kGwTile + i * 64 * 128;
-        if (kGwMt * k + j + 4 * i >= p.n_mtiles) {   // rows past the last m-tile
+        const uint32_t lo = o_lo + s * kGwTile + 2 * i * kGwHalf, hi = o_hi + s * kGwTile + 2 * i * kGwHalf;
+        const int c = c0 + 2 * i;
+        if (kGwMt * k + j >= p.n_mtiles) {   // rows past the last m-tile
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             sts128(lo + h * kGwHalf, 0u, 0u, 0u, 0u);
@@ -1065,28 +1052,34 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
         } else if (c + 1 < p.rows.n_res) {
           store_pair<GP>(raw[i], p.rows.sc_res, lo, hi);
         } else {
-          store_chunk<GP>(p.rows, raw[i], c, 0, lo, hi);
+          if (c < p.chunks) store_chunk<GP>(p.rows, raw[i], c, 0, lo, hi);
           if (c + 1 < p.chunks) store_chunk<GP>(p.rows, raw[i], c + 1, 1, lo, hi);
         }
         load(raw[i], i);
       }
-      filled();
-      b += kGwSets;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(wfull + 8 * s);
+      s += kGwSets;
+      if (s >= kGwStages) {
+        s -= kGwStages;
+        ph ^= 1u;
+      }
     }
-    // The accumulators: lane quarter w % 4 (tokens), every fourth piece of 32
+    // The accumulator: lane quarter w % 4 (tokens), every fourth piece of 32
     // columns.  A lane's 32 columns are two runs of the dequantising lanes' 16:
     // float4 (h, st) of them is operand columns 16 st + 4 (2 half + h) of the chunk.
-    if (warp_wait(flag, done, 0u, p.status) && 32 * j < p.T) {
+    const int quarter = warp & 3;
+    if (warp_wait(flag, done, 0u, p.status) && 32 * quarter < p.T) {
       tc_fence_after();
-      const int t = 32 * j + lane;
-      float* dx = p.dx + split * p.split_stride + static_cast<size_t>(t) * p.rows.Kc;
-      for (int piece = set; piece < 4 * nbl; piece += kGwSets) {
-        const int c = c0 + cstep * (piece >> 2) + (piece >> 1 & 1);
+      const int t = 32 * quarter + lane;
+      float* dx = p.dx + split * p.split_stride + static_cast<size_t>(t) * p.rows.Kc + c0 * 64;
+      for (int piece = warp >> 2; piece < 2 * nc; piece += 4) {
         uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + (static_cast<uint32_t>(32 * j) << 16) + 32 * piece, r);
+        tmem_ld_32x32b_x32(tbase + (static_cast<uint32_t>(32 * quarter) << 16) + 32 * piece, r);
         tmem_ld_wait();
-        if (t < p.T && c < p.chunks) {
-          float* dst = dx + c * 64 + (piece & 1) * 8;
+        if (t < p.T) {
+          float* dst = dx + (piece >> 1) * 64 + (piece & 1) * 8;
 #pragma unroll
           for (int st = 0; st < 4; ++st)
 #pragma unroll
@@ -1107,7 +1100,7 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
     const bool has_g = 32 * q < p.T;
     const int nq = (p.T + 31) / 32;
     const uint4* gsrc = p.G + (static_cast<size_t>(k0) * nq + q) * (kGwRows / 8 * 32) + lane;
-    const uint32_t gdst = tbase + (static_cast<uint32_t>(32 * q) << 16) + 128 * kGwBlocks;
+    const uint32_t gdst = tbase + (static_cast<uint32_t>(32 * q) << 16) + kGwCols;
     int gi = 0;
     uint32_t gv[4][16];
     auto g_load = [&]() {
@@ -1140,40 +1133,32 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
       if (has_g)
         while (gi < steps && g_put()) {}
     } else {
-    // (running values and immediate offsets only, as in g_mma_warp)
-    const uint64_t bd0 = smem_desc_mn128(tiles, kGwHalf);
-    constexpr uint32_t kFull = tc_idesc_f16(128, 128) | kTcIdescBmn;
-    // of the last block, whose second chunk may not exist
-    const uint32_t last_desc = c0 + cstep * (nbl - 1) + 1 < p.chunks ? kFull : tc_idesc_f16(128, 64) | kTcIdescBmn;
-    const uint32_t a0 = tbase + 128 * kGwBlocks;
-    uint64_t bd = bd0;
-    uint32_t ad = a0, wf = wfull, we = wempty, wph = 0, gf = gfull, ge = gempty, gph = 0;
-    uint32_t acc = 0;
-    bool ok = !has_g || g_put();
-    for (int k = 0; k < steps && ok; ++k) {
-      ok = warp_wait(flag, gf, gph, p.status);
-      if (!ok) break;
-      uint32_t d = tbase;
-      for (int b = 0; b < nbl; ++b) {
-        ok = warp_wait(flag, wf, wph, p.status);
+      // (running values and immediate offsets only, as in g_mma_warp)
+      const uint64_t bd0 = smem_desc_mn128(tiles, kGwHalf);
+      const uint32_t idesc = tc_idesc_f16(128, 64 * nc) | kTcIdescBmn;
+      const uint32_t a0 = tbase + kGwCols;
+      uint64_t bd = bd0;
+      uint32_t ad = a0, wf = wfull, we = wempty, wph = 0, gf = gfull, ge = gempty, gph = 0;
+      uint32_t acc = 0;
+      bool ok = !has_g || g_put();
+      for (int k = 0; k < steps && ok; ++k) {
+        ok = warp_wait(flag, gf, gph, p.status) && warp_wait(flag, wf, wph, p.status);
         if (!ok) break;
         tc_fence_after();
-        const bool last = b == nbl - 1;
-        const uint32_t idesc = last ? last_desc : kFull;
         if (elect_one()) {
-          tc_mma_ts(d, ad, bd, idesc, acc);
-          tc_mma_ts(d, ad + 8, bd + 128, idesc, 1u);
-          tc_mma_ts(d, ad + 16, bd + 256, idesc, 1u);
-          tc_mma_ts(d, ad + 24, bd + 384, idesc, 1u);
-          tc_mma_ts(d, ad + 32, bd + 512, idesc, 1u);
-          tc_mma_ts(d, ad + 40, bd + 640, idesc, 1u);
-          tc_mma_ts(d, ad + 48, bd + 768, idesc, 1u);
-          tc_mma_ts(d, ad + 56, bd + 896, idesc, 1u);
+          tc_mma_ts(tbase, ad, bd, idesc, acc);
+          tc_mma_ts(tbase, ad + 8, bd + 128, idesc, 1u);
+          tc_mma_ts(tbase, ad + 16, bd + 256, idesc, 1u);
+          tc_mma_ts(tbase, ad + 24, bd + 384, idesc, 1u);
+          tc_mma_ts(tbase, ad + 32, bd + 512, idesc, 1u);
+          tc_mma_ts(tbase, ad + 40, bd + 640, idesc, 1u);
+          tc_mma_ts(tbase, ad + 48, bd + 768, idesc, 1u);
+          tc_mma_ts(tbase, ad + 56, bd + 896, idesc, 1u);
           tc_commit(we);
-          if (last) tc_commit(ge);
+          tc_commit(ge);
         }
         __syncwarp();
-        d += 128;
+        acc = 1;
         bd += kGwTile >> 4;
         wf += 8;
         we += 8;
@@ -1183,23 +1168,20 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
           we = wempty;
           wph ^= 1u;
         }
-        // its own share of the next k-step, when this one's first MMAs are queued
-        if (b == 0 && has_g && gi < steps) ok = g_put();
-        if (!ok) break;
+        ad += kGwRows / 2;
+        gf += 8;
+        ge += 8;
+        if (gf == gempty) {
+          ad = a0;
+          gf = gfull;
+          ge = gempty;
+          gph ^= 1u;
+        }
+        // its own share of the next k-step, when this one's MMAs are queued
+        if (has_g && gi < steps) ok = g_put();
       }
-      acc = 1;
-      ad += kGwRows / 2;
-      gf += 8;
-      ge += 8;
-      if (gf == gempty) {
-        ad = a0;
-        gf = gfull;
-        ge = gempty;
-        gph ^= 1u;
-      }
-    }
-    if (ok && elect_one()) tc_commit(done);
-    __syncwarp();
+      if (ok && elect_one()) tc_commit(done);
+      __syncwarp();
     }
   }
   tc_fence_before();
@@ -1215,25 +1197,27 @@ constexpr int kFewTokens = 128;   // up to here the packed rows are dequantised 
 
 // Work split of gw_kernel.
 struct GwPlan {
-  int chunks, groups, big, s_big, s_small, nk;
+  int chunks, nk, grid;
+  GwSplits s;
 };
 GwPlan gw_plan(const archead_handle& h) {
   GwPlan g{};
   g.chunks = tc_kc(h.L) / 64;
   g.nk = (h.L.n_mtiles + kGwMt - 1) / kGwMt;
-  const int blocks = (g.chunks + 1) / 2;
-  // Three blocks per CTA read G least; fewer where the head is too small to
-  // give every SM a few tiles.  Groups of nb and nb - 1 blocks, with row splits
-  // in proportion: every CTA has about the same number of tiles.
-  int nb = std::min(kGwBlocks, blocks);
-  while (nb > 1 && static_cast<int64_t>((blocks + nb - 1) / nb) * g.nk < 4 * h.num_sms) --nb;
-  g.groups = (blocks + nb - 1) / nb;
-  g.big = g.groups - (g.groups * nb - blocks);
-  const auto share = [&](int b) {
-    return std::max(1, std::min(g.nk, static_cast<int>(static_cast<int64_t>(h.num_sms) * b / blocks)));
-  };
-  g.s_big = share(nb);
-  g.s_small = share(std::max(1, nb - 1));
+  const int blocks = (g.chunks + kGwChunks - 1) / kGwChunks, last = g.chunks - (blocks - 1) * kGwChunks;
+  g.s.res = h.L.n_res / kGwChunks;
+  g.s.rest = blocks - g.s.res;
+  // Row splits in proportion to a block's cost, so that the CTAs end together
+  // (measured at 151936 x 4096, 64 tokens: 0.91 us a tile of residual columns,
+  // 1.2 of INT5 codes, which take more unpacking, 0.72 of a single chunk, which
+  // has the same barriers).
+  const double rest = 1.25, tail = g.s.rest > 0 ? 0.65 + 0.15 * last : 0.0;
+  const double total = g.s.res + rest * std::max(0, g.s.rest - 1) + tail;
+  const auto share = [&](double cost) { return std::max(1, std::min(g.nk, static_cast<int>(h.num_sms * cost / total))); };
+  g.s.s_res = share(1.0);
+  g.s.s_rest = share(rest);
+  g.s.s_last = share(tail);
+  g.grid = g.s.res * g.s.s_res + (g.s.rest > 0 ? (g.s.rest - 1) * g.s.s_rest + g.s.s_last : 0);
   return g;
 }
 
@@ -1286,7 +1270,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.n_ssum = (L.n_mtiles + kGwMt - 1) / kGwMt;
     if (!use_tc(h, T)) o.logits = take(t * L.V * 4);
     const GwPlan g = gw_plan(h);
-    o.splits = std::max(g.s_big, g.s_small);
+    o.splits = std::max(g.s.s_res, std::max(g.s.s_rest, g.s.s_last));
   } else {
     const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * t)));
     const int n_chunks = static_cast<int>((L.Vp + rows - 1) / rows);
@@ -1410,12 +1394,12 @@ int grad_lowrank(const GradCall& c) {
 }
 
 // dX -> dh of one pass's tokens.
-int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, int splits_small, int groups, int big) {
+int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const GwSplits& gw) {
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
   DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, nt, Kc, L.d,
-              L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, splits_small, groups, big};
+              L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
   cudaError_t e = launch_after(dx_kernel, dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream, dp);
   CUtensorMap mz{}, mr{};
   if (e == cudaSuccess && Kz > 0) {
@@ -1459,18 +1443,14 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   w.n_mtiles = L.n_mtiles;
   w.nk = g.nk;
   w.chunks = g.chunks;
-  w.groups = g.groups;
-  w.big = g.big;
-  w.s_big = g.s_big;
-  w.s_small = g.s_small;
+  w.splits = g.s;
   w.dx = p.dx;
   w.split_stride = p.split_stride;
   w.status = p.status;
-  const int grid = g.big * g.s_big + (g.groups - g.big) * g.s_small;
   const auto kernel = w.rows.g_log2 >= 7 ? gw_kernel<1> : w.rows.g_log2 == 6 ? gw_kernel<2> : w.rows.g_log2 == 5 ? gw_kernel<4> : gw_kernel<8>;
-  e = launch_after(kernel, dim3(grid), kGwWarps * 32, kGwSmem, c.stream, w);
+  e = launch_after(kernel, dim3(g.grid), kGwWarps * 32, kGwSmem, c.stream, w);
   if (e != cudaSuccess) return set_cuda_error(e);
-  return grad_finish(c, p, n_ssum, g.s_big, g.s_small, g.groups, g.big);
+  return grad_finish(c, p, n_ssum, 0, g.s);
 }
 
 // Many tokens: chunk by chunk through the dequantised rows.
@@ -1511,7 +1491,7 @@ int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
     e = launch_gemm<kAccumulate>(p, mg, mwn, h.num_sms, c.stream);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
-  return grad_finish(c, p, o.n_ssum, o.splits, o.splits, 1, 1);
+  return grad_finish(c, p, o.n_ssum, o.splits, GwSplits{});
 }
 
 int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T, const int32_t* targets,
