@@ -1193,7 +1193,12 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
 }
 
 // -------------------------------------------------------------------- host
-constexpr int kFewTokens = 128;   // up to here the packed rows are dequantised inside the second product
+// Few tokens: the packed rows are dequantised inside the second product,
+// kFewPass tokens a pass over the head.  One such pass beats the chunks of W~ at
+// any head size; two do while the fp16 rows of the head are more than one chunk
+// (151936 x 4096: 0.78 ms at 129 tokens, 1.0 at 256, against 1.09; with the rows
+// in one chunk, 65531 x 1024: 160 to 198 us against 142).
+constexpr int kFewPass = 128;
 
 // Work split of gw_kernel.
 struct GwPlan {
@@ -1260,19 +1265,20 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     at += round_up(bytes, 256);
     return r;
   };
-  o.few = T <= kFewTokens;
-  const size_t t = o.few ? T : std::min(T, kGradTokens);
+  const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * std::min(T, kGradTokens))));
+  o.few = T <= kFewPass || (T <= 2 * kFewPass && static_cast<size_t>(L.Vp) > rows);
+  const int passes = (T + kFewPass - 1) / kFewPass;
+  const size_t t = o.few ? (T + passes - 1) / passes : std::min(T, kGradTokens);
   o.tokens = static_cast<int>(t);
   if (o.few) {
     // The forward call's workspace comes first: its header is this one's.
-    o.fwd = ws_layout(h, T).total;
+    o.fwd = ws_layout(h, o.tokens).total;
     at = round_up(o.fwd, 256);
     o.n_ssum = (L.n_mtiles + kGwMt - 1) / kGwMt;
-    if (!use_tc(h, T)) o.logits = take(t * L.V * 4);
+    if (!use_tc(h, 1 + o.tokens / 2)) o.logits = take(t * L.V * 4);   // (some pass may take the decode kernel)
     const GwPlan g = gw_plan(h);
     o.splits = std::max(g.s.s_res, std::max(g.s.s_rest, g.s.s_last));
   } else {
-    const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * t)));
     const int n_chunks = static_cast<int>((L.Vp + rows - 1) / rows);
     o.chunk = static_cast<int>(round_up((L.Vp + n_chunks - 1) / n_chunks, kGN));
     o.pitch = o.chunk + 64;   // (a power of two between G's rows would send a whole box to one memory channel)
