@@ -301,11 +301,12 @@ ARCHEAD_API int archead_merge_sample_shards(const float* sample_partials, int32_
  *   grad_hidden [T, d], 16-byte aligned, bf16 bit patterns or fp32 by
  *               grad_dtype; every row is written.
  * A target outside [0, V) with g != 0 gives a row of NaN and sets
- * ARCHEAD_STATUS_BAD_TARGET.  lse must be the log-sum-exp of the same head and
- * hidden state: one that is too small by log 2 or more gives NaN.  On a
- * vocabulary shard lse is the log-sum-exp over all rows (archead_merge_shards)
- * and targets are global: the result is this shard's share, to be added over
- * the shards (in fp32).
+ * ARCHEAD_STATUS_BAD_TARGET.  The probabilities are normalised by their own sum,
+ * so lse may be that of any of the forward calls; one that is off by log 2 or
+ * more may give NaN.  On a vocabulary shard (archead_set_vocab_shard with more
+ * rows than this head's) that sum is not known: lse is the log-sum-exp over all
+ * rows (archead_merge_shards), taken as it is, targets are global, and the
+ * result is this shard's share, to be added over the shards (in fp32).
  * workspace: >= archead_grad_workspace_bytes(handle, T), 256-byte aligned; the
  * call needs nothing in it and leaves its own status bits in the status word
  * (archead_workspace_status).  Calls that may overlap need one each. */

@@ -1275,7 +1275,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.fwd = ws_layout(h, o.tokens).total;
     at = round_up(o.fwd, 256);
     o.n_ssum = (L.n_mtiles + kGwMt - 1) / kGwMt;
-    if (!use_tc(h, 1 + o.tokens / 2)) o.logits = take(t * L.V * 4);   // (some pass may take the decode kernel)
+    if (!use_tc(h, o.tokens)) o.logits = take(t * L.V * 4);
     const GwPlan g = gw_plan(h);
     o.splits = std::max(g.s.s_res, std::max(g.s.s_rest, g.s.s_last));
   } else {

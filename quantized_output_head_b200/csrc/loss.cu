@@ -34,7 +34,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "device.cuh"
 #include "handle.h"
@@ -633,22 +632,17 @@ LossLayout loss_layout(int S) {
   return o;
 }
 
-// Blocks of a call: a warp's run is one group of tokens while that many blocks
-// fit.  Also sets up the device on its first call (clusters of more than 8
-// blocks are opted into).
-struct LossDevice {
-  std::once_flag once;
-  int sms = 0;
-  cudaError_t error = cudaSuccess;
-};
-constexpr int kMaxDevices = 64;
-LossDevice g_loss_device[kMaxDevices];
-
-int loss_blocks(int T, int sms) {
-  if (T > kOneCluster) return std::min(sms, kLossMaxBlocks);
-  int b = 1;
-  while (T > b * kOneBlock) b *= 2;
-  return b;
+// Blocks of a call: a warp's run is one group of tokens while that many fit.
+int loss_blocks(int T, int* blocks) {
+  *blocks = 1;
+  while (*blocks < 16 && T > *blocks * kOneBlock) *blocks *= 2;
+  if (T <= kOneCluster) return ARCHEAD_OK;
+  int dev = -1, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  *blocks = std::max(16, std::min(sms, kLossMaxBlocks));
+  return ARCHEAD_OK;
 }
 
 void token_args(TokenArgs& a, const float* ce, const float* ce_ref, const uint8_t* mask, const int32_t* cu, int T, int S,
@@ -687,24 +681,6 @@ constexpr LossKernels<PolicyArgs> kPolicy{policy_loss_kernel<kMeetBlock>, policy
 constexpr LossKernels<PreferenceArgs> kPreference{preference_loss_kernel<kMeetBlock>, preference_loss_kernel<kMeetCluster>,
                                                   preference_loss_kernel<kMeetGrid>};
 
-int loss_device(int* sms) {
-  int dev = -1;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return set_cuda_error(e);
-  if (dev < 0 || dev >= kMaxDevices) return ARCHEAD_EUNSUP;
-  LossDevice& d = g_loss_device[dev];
-  std::call_once(d.once, [&]() {
-    d.error = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (d.error == cudaSuccess)
-      d.error = cudaFuncSetAttribute(kPolicy.cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (d.error == cudaSuccess)
-      d.error = cudaFuncSetAttribute(kPreference.cluster, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (d.error != cudaSuccess) return set_cuda_error(d.error);
-  *sms = d.sms;
-  return ARCHEAD_OK;
-}
-
 template <class Args>
 int launch_loss(const LossKernels<Args>& kernels, const Args& args, int blocks, archead_stream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -713,19 +689,22 @@ int launch_loss(const LossKernels<Args>& kernels, const Args& args, int blocks, 
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   void (*kernel)(Args) = kernels.block;
+  cudaError_t e = cudaSuccess;
   if (blocks > 16) {
     kernel = kernels.grid;
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
   } else if (blocks > 1) {
     kernel = kernels.cluster;
+    // clusters of more than 8 blocks are opted into (per context, so at every call)
+    if (blocks > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = blocks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   }
   cfg.attrs = attr;
   cfg.numAttrs = blocks > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, args);
   return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
 }
 
@@ -762,10 +741,9 @@ extern "C" ARCHEAD_API int archead_policy_loss(const float* ce, const float* ce_
     if (!aligned(q, 4)) return ARCHEAD_EALIGN;
   if (!aligned(workspace, 256)) return ARCHEAD_EALIGN;
   if (workspace_bytes < loss_layout(n_sequences).total) return ARCHEAD_ENOMEM;
-  int sms = 0;
-  const int rc = loss_device(&sms);
+  int blocks = 1;
+  const int rc = loss_blocks(T, &blocks);
   if (rc != ARCHEAD_OK) return rc;
-  const int blocks = loss_blocks(T, sms);
   PolicyArgs p{};
   token_args(p.a, ce, ce_ref, mask, cu_seqlens, T, n_sequences, grad_ce, workspace, blocks);
   if (!aligned(ce_old, 16) || (!per_sequence && !aligned(advantages, 16))) p.a.vec = 0;
@@ -805,10 +783,9 @@ extern "C" ARCHEAD_API int archead_preference_loss(const float* ce, const float*
     if (!aligned(q, 4)) return ARCHEAD_EALIGN;
   if (!aligned(workspace, 256)) return ARCHEAD_EALIGN;
   if (workspace_bytes < loss_layout(2 * n_pairs).total) return ARCHEAD_ENOMEM;
-  int sms = 0;
-  const int rc = loss_device(&sms);
+  int blocks = 1;
+  const int rc = loss_blocks(T, &blocks);
   if (rc != ARCHEAD_OK) return rc;
-  const int blocks = loss_blocks(T, sms);
   PreferenceArgs p{};
   token_args(p.a, ce, ce_ref, mask, cu_seqlens, T, 2 * n_pairs, grad_ce, workspace, blocks);
   p.beta = o.beta;
