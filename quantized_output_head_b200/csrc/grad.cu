@@ -49,9 +49,10 @@ namespace {
 
 constexpr int kGradTokens = 4096;     // tokens of one pass over the head
 // Vocabulary rows of one pass: as many as keep the W~ chunk and the G chunk near
-// these sizes (16,640 rows at 4096 tokens and 4672 columns; fewer passes re-read
-// and re-write dX less often, and leave fewer part-filled rounds of tiles).
-constexpr size_t kGradWBytes = size_t(160) << 20, kGradGBytes = size_t(256) << 20;
+// these sizes (35,840 rows at 4096 tokens and 4672 columns).  Fewer passes re-read
+// and re-write dX less often and leave fewer part-filled rounds of tiles: 29, 17,
+// 9 and 5 passes took 9.1, 8.5, 8.2 and 7.9 ms for the chunks' kernels.
+constexpr size_t kGradWBytes = size_t(320) << 20, kGradGBytes = size_t(512) << 20;
 constexpr int kGradScale = kTcGradScale;   // G is stored times 2^15
 
 // ------------------------------------------------------------ packed -> fp16
@@ -150,6 +151,7 @@ struct LowrankParams {
   const int8_t* B;
   const uint16_t* s_B;
   uint16_t* out;
+  uint16_t* out_perm;         // or null: the same rows, columns in the operand order (z of heads without act_prep)
   uint32_t* header;           // 64 words of the workspace: status, tickets
   int32_t d, rcp, rrp, Kz, g_B;
   float mul_c, mul_r;
@@ -181,35 +183,42 @@ __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p
     }
   }
   *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(e) * p.d + j) = make_uint4(o[0], o[1], o[2], o[3]);
+  if (p.out_perm != nullptr) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint32_t*>(p.out_perm + static_cast<size_t>(e) * p.d + (j & ~15) + tc_kpos((j & 15) + 2 * c)) = o[c];
+  }
 }
 
-// X of heads whose z the activation kernel does not compute (g_B not a multiple
-// of 64), from the decode prologue's z pairs.
+// The h columns of X, and 2^-c_t, for heads whose z the activation kernel does
+// not compute (g_B not a multiple of 64); their z columns come from a product
+// with the fp16 rows of R and B (1769 x 2176 with 512 + 512 rows, g_B = 32, 2708
+// tokens: 0.16 ms for the whole gradient; with the decode path's z kernel, 8
+// tokens a pass over R and B, 2.4).  One block per token.
 struct XParams {
   const uint16_t* hidden;
-  const uint16_t* zhi;
-  const uint16_t* zlo;
-  const int32_t* escale;
   uint16_t* xop;
   float* cinv;
-  int32_t d, rcp, Kz, Kc, alpha, beta, gamma, mseg, e_B;
+  int32_t d, Kc, alpha, mseg;
 };
-__global__ void __launch_bounds__(256) x_from_z_kernel(const XParams p) {
-  const int t = blockIdx.x, E = p.escale[t];
+__global__ void __launch_bounds__(128) x_hidden_kernel(const XParams p) {
+  __shared__ uint32_t part[4];
+  const int t = blockIdx.x;
+  const uint16_t* h = p.hidden + static_cast<size_t>(t) * p.d;
+  uint32_t m = 0;
+  for (int j = threadIdx.x; j < p.d; j += 128) m = max(m, static_cast<uint32_t>(h[j]) & 0x7FFFu);   // |bf16| orders like its bits
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+  m = max(max(part[0], part[1]), max(part[2], part[3]));
+  int E = 0;
+  if (m != 0) frexpf(__uint_as_float(m << 16), &E);   // max|h_t| < 2^E
   if (threadIdx.x == 0) p.cinv[t] = ldexpf(1.f, E - kScaleExp - p.mseg);
-  const float sh = ldexpf(1.f, kScaleExp - E + p.mseg - p.alpha);
-  const float sc = ldexpf(1.f, p.e_B + p.mseg - p.beta), sr = ldexpf(1.f, p.e_B + p.mseg - p.gamma);
-  for (int e = threadIdx.x; e < p.Kc; e += blockDim.x) {
+  const float s = ldexpf(1.f, kScaleExp - E + p.mseg - p.alpha);
+  for (int e = threadIdx.x; e < p.d; e += 128) {
     const int k = (e & ~15) + tc_kcol(e & 15);
-    float v = 0.f;
-    if (k < p.d) {
-      v = __uint_as_float(static_cast<uint32_t>(p.hidden[static_cast<size_t>(t) * p.d + k]) << 16) * sh;
-    } else if (k - p.d < p.Kz) {
-      const size_t i = static_cast<size_t>(t) * p.Kz + (k - p.d);
-      const float z = __half2float(__ushort_as_half(p.zhi[i])) + __half2float(__ushort_as_half(p.zlo[i]));
-      v = z * (k - p.d < p.rcp ? sc : sr);
-    }
-    p.xop[static_cast<size_t>(t) * p.Kc + e] = __half_as_ushort(__float2half_rn(v));
+    p.xop[static_cast<size_t>(t) * p.Kc + e] =
+        __half_as_ushort(__float2half_rn(__uint_as_float(static_cast<uint32_t>(h[k]) << 16) * s));
   }
 }
 
@@ -345,7 +354,7 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size
 
 // -------------------------------------------------------------------- gemm
 // D[256 tokens x 256 columns] tiles of A B, A [tokens][K] fp16 K-major, B fp16
-// either [columns][K] (softmax) or [K][columns] (accumulate, finish), by TMA in
+// either [columns][K] (softmax, lowrank) or [K][columns] (accumulate, finish), by TMA in
 // k-steps of 64, on pairs of CTAs: each holds the A rows of its 128 tokens and
 // half of B's columns, one tcgen05.mma of the leader multiplies both (the tensor
 // cores read their shared-memory operands at about 64 bytes a clock and SM; alone,
@@ -360,7 +369,8 @@ constexpr uint32_t kGTileOff = kGBarOff + 256;       // 32 x 33 words per epilog
 constexpr uint32_t kGSmem = kGTileOff + kGEpi * 32 * 33 * 4 + 1024;
 constexpr uint32_t kGTmem = 512;
 
-enum GemmMode { kSoftmax, kAccumulate, kFinish };
+enum GemmMode { kSoftmax, kLowrank, kAccumulate, kFinish };
+constexpr bool gemm_b_mn(GemmMode m) { return m == kAccumulate || m == kFinish; }   // B stored [K][columns]
 
 struct GemmParams {
   int32_t M, N;                        // tokens; columns of this product
@@ -378,6 +388,7 @@ struct GemmParams {
   int32_t pitch, v0, V;                // first row of the chunk, rows of the head
   float* ssum;                         // [tiles][2][tokens]: sums of exp(y - lse) over half a tile's rows
   int32_t tokens;
+  uint16_t* x;                         // lowrank: z columns of X, [M][Kc]
   // accumulate / finish
   float* dx;                           // [splits][M][Kc]
   size_t split_stride;
@@ -451,7 +462,7 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
   for (int i = 0; ok && g_unit(p, pair, pairs, i, w); ++i) {
     const int n0 = w.n * kGN + rank * (w.cols / 2);
     const int nb = w.cols / 128;   // 64-column boxes of B (stored [K][columns])
-    const uint32_t bytes = 2 * (kGABytes + (kMode == kSoftmax ? kGBBytes : nb * 8192u));   // of both CTAs
+    const uint32_t bytes = 2 * (kGABytes + (gemm_b_mn(kMode) ? nb * 8192u : kGBBytes));   // of both CTAs
     for (int k = w.k0; k < w.k1; ++k) {
       ok = g_wait(sm, sm.empty + 8 * s, ph ^ 1u, p.status);
       if (!ok) break;
@@ -460,7 +471,7 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
         const uint32_t bar = cluster_addr(sm.full + 8 * s, 0);   // the leader's
         if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * s, bytes);
         tma_load_2d_pair(a, ma, k * 64, w.m * kGM + rank * (kGM / 2), bar);
-        if constexpr (kMode == kSoftmax) {
+        if constexpr (!gemm_b_mn(kMode)) {
           tma_load_2d_pair(b, mb, k * 64, n0, bar);
         } else {
           for (int e = 0; e < nb; ++e) tma_load_2d_pair(b + e * 8192u, mb, n0 + 64 * e, k * 64, bar);
@@ -489,7 +500,7 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
 // is an immediate offset from running values that advance by constants.
 template <GemmMode kMode>
 __device__ void g_mma_warp(const GemmParams& p, const GemmSmem& sm, uint32_t tmem_base, int pair, int pairs) {
-  constexpr bool kMn = kMode != kSoftmax;
+  constexpr bool kMn = gemm_b_mn(kMode);
   constexpr uint32_t kBStep = kMn ? 128u : 2u;   // descriptor units per K = 16
   constexpr uint32_t kStep = kGStageBytes >> 4;
   constexpr uint32_t kDesc = tc_idesc_f16(kGM, kGN) | (kMn ? kTcIdescBmn : 0u);
@@ -566,7 +577,7 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
     const bool live = t < p.M;
     float g = 0.f, cinv = 0.f, lse = 0.f;
     int target = -1;
-    if (live && kMode != kAccumulate) {
+    if (live && (kMode == kSoftmax || kMode == kFinish)) {
       g = p.grad[t];
       target = p.targets[t];
       if constexpr (kMode == kSoftmax) {
@@ -624,6 +635,19 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
               const uint32_t* src = tile + row * 17 + 4 * v;
               *reinterpret_cast<uint4*>(p.G + static_cast<size_t>(t0 + row) * p.pitch + n0 + c0 + 8 * v) =
                   make_uint4(src[0], src[1], src[2], src[3]);
+            }
+          }
+        } else if constexpr (kMode == kLowrank) {
+          // z columns of X
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(p.x + static_cast<size_t>(t) * p.Kc + n0 + c0);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[e] = pack_half2(__uint_as_float(r[8 * v + 2 * e]) * p.mul_acc, __uint_as_float(r[8 * v + 2 * e + 1]) * p.mul_acc);
+              dst[v] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
         } else if constexpr (kMode == kAccumulate) {
@@ -1196,7 +1220,7 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
 // Few tokens: the packed rows are dequantised inside the second product,
 // kFewPass tokens a pass over the head.  One such pass beats the chunks of W~ at
 // any head size; two do while the fp16 rows of the head are more than one chunk
-// (151936 x 4096: 0.78 ms at 129 tokens, 1.0 at 256, against 1.09; with the rows
+// (151936 x 4096: 0.78 ms at 129 tokens, 1.0 at 256, against 1.1; with the rows
 // in one chunk, 65531 x 1024: 160 to 198 us against 142).
 constexpr int kFewPass = 128;
 
@@ -1251,7 +1275,7 @@ struct GradLayout {
   bool few;
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
   int pitch, n_ssum;
-  size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, escale, zhi, zlo, total;
+  size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, rbp, total;
 };
 
 GradLayout grad_layout(const archead_handle& h, int T) {
@@ -1266,7 +1290,8 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     return r;
   };
   const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * std::min(T, kGradTokens))));
-  o.few = T <= kFewPass || (T <= 2 * kFewPass && static_cast<size_t>(L.Vp) > rows);
+  // (without the tensor-core forward a pass of its logits takes 8 tokens)
+  o.few = h.tc_ok ? T <= kFewPass || (T <= 2 * kFewPass && static_cast<size_t>(L.Vp) > rows) : T <= kDecodeTokens;
   const int passes = (T + kFewPass - 1) / kFewPass;
   const size_t t = o.few ? (T + passes - 1) / passes : std::min(T, kGradTokens);
   o.tokens = static_cast<int>(t);
@@ -1293,58 +1318,9 @@ GradLayout grad_layout(const archead_handle& h, int T) {
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
   o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
-  if (!o.few && !h.tc_ok) {
-    o.escale = take(t * 4);
-    o.zhi = take(t * L.Kz * 2);
-    o.zlo = take(t * L.Kz * 2);
-  }
+  if (!o.few && !h.tc_ok) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 2);
   o.total = at;
   return o;
-}
-
-// X and 2^-c_t of one pass's tokens.
-cudaError_t grad_activations(const archead_handle& h, const GradLayout& o, const uint16_t* hidden, int T, uint8_t* wb,
-                             cudaStream_t stream) {
-  const Layout& L = h.L;
-  uint32_t* status = reinterpret_cast<uint32_t*>(wb + 4);
-  if (h.tc_ok) {
-    ActParams ap = act_params(h);
-    ap.hidden = hidden;
-    ap.status = status;
-    ap.xop = reinterpret_cast<uint16_t*>(wb + o.xop);
-    ap.cinv = reinterpret_cast<float*>(wb + o.cinv);
-    ap.T = T;
-    ap.zpart = reinterpret_cast<float*>(wb + o.dx);   // dX is written later
-    ap.zticket = reinterpret_cast<uint32_t*>(wb + kActTicketOff);
-    return launch_act_prep(ap, act_prep_splits(T, L.d, ap.Kc, h.num_sms, o.dz - o.dx), stream);
-  }
-  PrologueParams pp{};
-  pp.hidden = hidden;
-  pp.R = reinterpret_cast<const int8_t*>(h.arena + L.off_R);
-  pp.s_R = reinterpret_cast<const uint16_t*>(h.arena + L.off_sR);
-  pp.B = reinterpret_cast<const int8_t*>(h.arena + L.off_B);
-  pp.s_B = reinterpret_cast<const uint16_t*>(h.arena + L.off_sB);
-  pp.zhi = reinterpret_cast<uint16_t*>(wb + o.zhi);
-  pp.zlo = reinterpret_cast<uint16_t*>(wb + o.zlo);
-  pp.escale = reinterpret_cast<int32_t*>(wb + o.escale);
-  pp.counter = reinterpret_cast<uint32_t*>(wb);
-  pp.status = status;
-  pp.e_B = h.e_B;
-  pp.T = T;
-  pp.d = L.d;
-  pp.rcp = L.rcp;
-  pp.rrp = L.rrp;
-  pp.Kz = L.Kz;
-  pp.g_B = L.g_B;
-  pp.V = L.V;
-  pp.v_total = h.v_total;
-  cudaError_t e = launch_prologue(pp, stream);
-  if (e != cudaSuccess) return e;
-  XParams xp{hidden, pp.zhi, pp.zlo, pp.escale, reinterpret_cast<uint16_t*>(wb + o.xop),
-             reinterpret_cast<float*>(wb + o.cinv), L.d, L.rcp, L.Kz, tc_kc(L), h.tc_alpha, h.tc_beta, h.tc_gamma,
-             h.tc_mseg, h.e_B};
-  x_from_z_kernel<<<T, 256, 0, stream>>>(xp);
-  return cudaGetLastError();
 }
 
 DequantParams dequant_params(const archead_handle& h, uint16_t* out) {
@@ -1380,6 +1356,40 @@ struct GradCall {
   int sigma;                  // dz carries 2^beta (2^gamma), the rows of R (B) 2^rho: both meet in 2^sigma
 };
 
+// X and 2^-c_t of one pass's tokens.
+cudaError_t grad_activations(const GradCall& c, const uint16_t* hidden, GemmParams p) {
+  const archead_handle& h = c.h;
+  const Layout& L = h.L;
+  const int T = p.M, Kc = tc_kc(L);
+  uint16_t* xop = reinterpret_cast<uint16_t*>(c.wb + c.o.xop);
+  float* cinv = reinterpret_cast<float*>(c.wb + c.o.cinv);
+  if (h.tc_ok) {
+    ActParams ap = act_params(h);
+    ap.hidden = hidden;
+    ap.status = p.status;
+    ap.xop = xop;
+    ap.cinv = cinv;
+    ap.T = T;
+    ap.zpart = reinterpret_cast<float*>(c.wb + c.o.dx);   // dX is written later
+    ap.zticket = reinterpret_cast<uint32_t*>(c.wb + kActTicketOff);
+    return launch_act_prep(ap, act_prep_splits(T, L.d, Kc, h.num_sms, c.o.dz - c.o.dx), c.stream);
+  }
+  x_hidden_kernel<<<T, 128, 0, c.stream>>>(XParams{hidden, xop, cinv, L.d, Kc, h.tc_alpha, h.tc_mseg});
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || c.o.Kz == 0) return e;
+  // z = h [R | B]^T: the operand's h carries 2^(c_t - alpha), the rows 2^(sigma - beta|gamma)
+  CUtensorMap mx, mr;
+  e = tc_encode_map(&mx, xop, L.d, T, Kc, kGM / 2);
+  if (e == cudaSuccess) e = tc_encode_map(&mr, reinterpret_cast<const uint16_t*>(c.wb + c.o.rbp), L.d, c.o.Kz, L.d, kGN / 2);
+  if (e != cudaSuccess) return e;
+  p.N = c.o.Kz;
+  p.n_k = L.d / 64;
+  p.splits = 1;
+  p.x = xop + L.d;
+  p.mul_acc = std::ldexp(1.f, h.tc_alpha - c.sigma);
+  return launch_gemm<kLowrank>(p, mx, mr, h.num_sms, c.stream);
+}
+
 // The rows of R and B for the last product; the header cleared (status word,
 // tickets of the activation kernel).
 int grad_lowrank(const GradCall& c) {
@@ -1392,7 +1402,9 @@ int grad_lowrank(const GradCall& c) {
                    reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sR),
                    reinterpret_cast<const int8_t*>(c.h.arena + L.off_B),
                    reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sB),
-                   reinterpret_cast<uint16_t*>(c.wb + c.o.rb), reinterpret_cast<uint32_t*>(c.wb), L.d, L.rcp, L.rrp, c.o.Kz, L.g_B,
+                   reinterpret_cast<uint16_t*>(c.wb + c.o.rb),
+                   c.o.rbp != 0 ? reinterpret_cast<uint16_t*>(c.wb + c.o.rbp) : nullptr,
+                   reinterpret_cast<uint32_t*>(c.wb), L.d, L.rcp, L.rrp, c.o.Kz, L.g_B,
                    std::ldexp(1.f, c.sigma - c.h.tc_beta), std::ldexp(1.f, c.sigma - c.h.tc_gamma)};
   lowrank_rows_kernel<<<(c.o.Kz * (L.d / 8) + 255) / 256, 256, 0, c.stream>>>(lp);
   const cudaError_t e = cudaGetLastError();
@@ -1466,7 +1478,7 @@ int grad_many(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   const GradLayout& o = c.o;
   const int Kc = tc_kc(L), nt = p.M;
   uint16_t* w = reinterpret_cast<uint16_t*>(c.wb + o.w);
-  cudaError_t e = grad_activations(h, o, hidden, nt, c.wb, c.stream);
+  cudaError_t e = grad_activations(c, hidden, p);
   if (e != cudaSuccess) return set_cuda_error(e);
   DequantParams dq = dequant_params(h, w);
   p.cinv = reinterpret_cast<const float*>(c.wb + o.cinv);
@@ -1539,6 +1551,8 @@ constexpr int kMaxTokens = 1 << 20;
 
 cudaError_t grad_set_attributes() {
   cudaError_t e = cudaFuncSetAttribute(grad_gemm_kernel<kSoftmax>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(grad_gemm_kernel<kLowrank>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(grad_gemm_kernel<kAccumulate>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
