@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p
   }
 }
 
-// The h columns of X, and 2^-c_t, for heads whose z the activation kernel does
-// not compute (g_B not a multiple of 64); their z columns come from a product
-// with the fp16 rows of R and B (1769 x 2176 with 512 + 512 rows, g_B = 32, 2708
+// The h columns of X, and 2^-c_t, where the activation kernel is not used (many
+// tokens; heads with g_B not a multiple of 64, which it does not take); the z
+// columns come from a product with the fp16 rows of R and B (1769 x 2176 with 512 + 512 rows, g_B = 32, 2708
 // tokens: 0.16 ms for the whole gradient; with the decode path's z kernel, 8
 // tokens a pass over R and B, 2.4).  One block per token.
 struct XParams {
@@ -268,68 +268,80 @@ __host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) 
   return block < g.res ? g.s_res : block + 1 < g.res + g.rest ? g.s_rest : g.s_last;
 }
 
-// Blocks of 1024 columns per token: S from the tiles' partial sums (in a fixed order), then
-// dX (added over the K splits) / S + (1/S - 1) W~[target]; the residual columns
-// stay fp32 in the first split's place, the low-rank ones become the fp16
-// operand dz [T][Kz'].
+// Blocks of 1024 columns per token: S from the tiles' partial sums (in a fixed
+// order), then dX (added over the K splits) / S + (1/S - 1) W~[target]; the
+// residual columns stay fp32 in the first split's place, the low-rank ones become
+// the fp16 operand dz [T][Kz'].  Latency is all there is to it at few tokens: the
+// loads are issued in batches, a token's partial sums lie side by side, and the
+// target's row is read before the wait (16 tokens of 262144 x 2560: 21 -> 6 us).
 struct DxParams {
   DequantParams rows;
-  const float* ssum;          // [n_ssum][tokens]
+  const float* ssum;          // [tokens][ssum_pitch], n_ssum of them used
   const float* grad;
   const int32_t* targets;
   float* dx;
   size_t split_stride;
   uint16_t* dz;
-  int32_t n_ssum, tokens, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
+  int32_t n_ssum, ssum_pitch, Kc, d, V, row0, whole;   // whole: all rows of the vocabulary are here
   int32_t splits;                                  // partial dX of every column, or (0) by
   GwSplits gw;
 };
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   __shared__ float part[8];
+  // What the call was given may be read before the wait: the call's first kernel
+  // is not a dependent launch.
+  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = blockIdx.y * 256 + threadIdx.x;
+  const bool in = q < p.Kc / 4, live = p.grad[t] != 0.f;   // (else its row of dX is zero, S has no meaning)
+  const int target = p.whole && live ? p.targets[t] - p.row0 : -1;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in && target >= 0 && target < p.V)
+    w = packed_row4(p.rows, p.rows.mtiles + static_cast<size_t>(target / kMT) * p.rows.mblk_bytes, target % kMT, q);
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q0 = blockIdx.y * blockDim.x + threadIdx.x, dq = gridDim.y * blockDim.x;
-  if (p.grad[t] == 0.f) {     // its row of dX is zero, S has no meaning
-    for (int q = q0; q < (p.Kc - p.d) / 4; q += dq)
-      *reinterpret_cast<uint2*>(p.dz + static_cast<size_t>(t) * (p.Kc - p.d) + 4 * q) = make_uint2(0u, 0u);
+  float4* dx = reinterpret_cast<float4*>(p.dx + static_cast<size_t>(t) * p.Kc) + q;
+  uint2* dz = reinterpret_cast<uint2*>(p.dz + static_cast<size_t>(t) * (p.Kc - p.d) + 4 * q - p.d);
+  if (!live) {
+    if (in && 4 * q >= p.d) *dz = make_uint2(0u, 0u);
     return;
+  }
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in) {
+    v = *dx;
+    const int n = p.splits > 0 ? p.splits : gw_splits(p.gw, 4 * q / kGwCols);
+#pragma unroll 8
+    for (int s = 1; s < n; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(dx) + s * p.split_stride);
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
   }
   float r = 1.f;
   if (p.whole) {
+    const float* parts = p.ssum + static_cast<size_t>(t) * p.ssum_pitch;
     float s = 0.f;
-    for (int i = threadIdx.x; i < p.n_ssum; i += blockDim.x) s += p.ssum[static_cast<size_t>(i) * p.tokens + t];
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.n_ssum / 4; i += 256) {
+      const float4 x = reinterpret_cast<const float4*>(parts)[i];
+      s += (x.x + x.y) + (x.z + x.w);
+    }
+    if (threadIdx.x < p.n_ssum % 4) s += parts[p.n_ssum - 1 - threadIdx.x];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) part[warp] = s;
     __syncthreads();
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w];
+    for (int i = 0; i < 8; ++i) s += part[i];
     r = 1.f / s;
   }
-  const int target = p.targets[t] - p.row0;
-  const bool has = p.whole && target >= 0 && target < p.V;
+  if (!in) return;
   const float c = (r - 1.f) * static_cast<float>(1 << kGradScale);
-  const uint8_t* blk = p.rows.mtiles + static_cast<size_t>(has ? target / kMT : 0) * p.rows.mblk_bytes;
-  float* dx = p.dx + static_cast<size_t>(t) * p.Kc;
-  for (int q = q0; q < p.Kc / 4; q += dq) {
-    float4 v = reinterpret_cast<const float4*>(dx)[q];
-    const int n = p.splits > 0 ? p.splits : gw_splits(p.gw, 4 * q / kGwCols);
-    for (int s = 1; s < n; ++s) {
-      const float4 x = reinterpret_cast<const float4*>(dx + s * p.split_stride)[q];
-      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
-    }
-    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (has) w = packed_row4(p.rows, blk, target % kMT, q);
-    v = make_float4(fmaf(c, w.x, v.x * r), fmaf(c, w.y, v.y * r), fmaf(c, w.z, v.z * r), fmaf(c, w.w, v.w * r));
-    if (4 * q < p.d) {
-      reinterpret_cast<float4*>(dx)[q] = v;
-    } else {
-      constexpr float kInv = 1.f / (1 << kGradScale);
-      *reinterpret_cast<uint2*>(p.dz + static_cast<size_t>(t) * (p.Kc - p.d) + 4 * q - p.d) =
-          make_uint2(pack_half2(v.x * kInv, v.y * kInv), pack_half2(v.z * kInv, v.w * kInv));
-    }
+  v = make_float4(fmaf(c, w.x, v.x * r), fmaf(c, w.y, v.y * r), fmaf(c, w.z, v.z * r), fmaf(c, w.w, v.w * r));
+  if (4 * q < p.d) {
+    *dx = v;
+  } else {
+    constexpr float kInv = 1.f / (1 << kGradScale);
+    *dz = make_uint2(pack_half2(v.x * kInv, v.y * kInv), pack_half2(v.z * kInv, v.w * kInv));
   }
 }
 
@@ -386,8 +398,8 @@ struct GemmParams {
   const float* lse;                    // [M]
   uint16_t* G;                         // [M][pitch]
   int32_t pitch, v0, V;                // first row of the chunk, rows of the head
-  float* ssum;                         // [tiles][2][tokens]: sums of exp(y - lse) over half a tile's rows
-  int32_t tokens;
+  float* ssum;                         // [tokens][ssum_pitch]: sums of exp(y - lse) over half a tile's rows
+  int32_t ssum_pitch;
   uint16_t* x;                         // lowrank: z columns of X, [M][Kc]
   // accumulate / finish
   float* dx;                           // [splits][M][Kc]
@@ -710,7 +722,7 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
         __syncwarp();
       }
       if (kMode == kSoftmax && live)
-        p.ssum[static_cast<size_t>(2 * (p.v0 / kGN + w.n) + half) * p.tokens + t] = ssum * (1.f / (1 << kGradScale));
+        p.ssum[static_cast<size_t>(t) * p.ssum_pitch + 2 * (p.v0 / kGN + w.n) + half] = ssum * (1.f / (1 << kGradScale));
       tc_fence_before();
     }
     __syncwarp();
@@ -802,8 +814,8 @@ struct GParams {
   const float* grad;
   const int32_t* targets;
   uint4* G;                   // [k-step][T / 32][16][32]
-  float* ssum;                // [k-step][T]
-  int32_t T, V, row0;
+  float* ssum;                // [T][ssum_pitch], one per k-step
+  int32_t T, V, row0, ssum_pitch;
 };
 constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
 __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
@@ -829,7 +841,7 @@ __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && t < p.T) p.ssum[static_cast<size_t>(blockIdx.x) * p.T + t] = sum;
+    if (lane == 0 && t < p.T) p.ssum[static_cast<size_t>(t) * p.ssum_pitch + blockIdx.x] = sum;
   }
   __syncthreads();
   uint4* dst = p.G + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * (kGwRows / 8 * 32);
@@ -1224,6 +1236,13 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
 // in one chunk, 65531 x 1024: 160 to 198 us against 142).
 constexpr int kFewPass = 128;
 
+// Many tokens of a head with low-rank rows: z by a product with the fp16 rows of
+// R and B from this many tokens on, below by the activation kernel, which has one
+// launch less (whole gradient, 151936 x 4096: 384 tokens 1741 against 1703 us,
+// 4096 tokens 9.74 against 9.88 ms; 32003 x 2048: 384 tokens 205 against 203 us,
+// 1024 324 against 333, 4096 1022 against 1117).
+constexpr int kOwnXTokens = 1024;
+
 // Work split of gw_kernel.
 struct GwPlan {
   int chunks, nk, grid;
@@ -1272,7 +1291,7 @@ int accumulate_splits(int tokens, int Kc, int chunk, int pairs) {
 }
 
 struct GradLayout {
-  bool few;
+  bool few, own_x;                 // own_x: X by x_hidden_kernel and a product
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
   int pitch, n_ssum;
   size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, rbp, total;
@@ -1309,16 +1328,17 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.pitch = o.chunk + 64;   // (a power of two between G's rows would send a whole box to one memory channel)
     o.n_ssum = 2 * ((L.Vp + kGN - 1) / kGN);
     o.splits = accumulate_splits(o.tokens, Kc, o.chunk, h.num_sms / 2);
+    o.own_x = !h.tc_ok || (o.Kz > 0 && t >= kOwnXTokens);
     o.cinv = take(t * 4);
     o.xop = take(t * Kc * 2);
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
   }
-  o.ssum = take((o.few ? 4 : 1) * o.n_ssum * t * 4);
+  o.ssum = take(t * (o.few ? 4 * o.n_ssum : round_up(o.n_ssum, 4)) * 4);
   o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
   o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
-  if (!o.few && !h.tc_ok) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 2);
+  if (o.own_x) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 2);
   o.total = at;
   return o;
 }
@@ -1363,7 +1383,7 @@ cudaError_t grad_activations(const GradCall& c, const uint16_t* hidden, GemmPara
   const int T = p.M, Kc = tc_kc(L);
   uint16_t* xop = reinterpret_cast<uint16_t*>(c.wb + c.o.xop);
   float* cinv = reinterpret_cast<float*>(c.wb + c.o.cinv);
-  if (h.tc_ok) {
+  if (!c.o.own_x) {
     ActParams ap = act_params(h);
     ap.hidden = hidden;
     ap.status = p.status;
@@ -1416,7 +1436,7 @@ int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const 
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
-  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, nt, Kc, L.d,
+  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
   cudaError_t e = launch_after(dx_kernel, dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream, dp);
   CUtensorMap mz{}, mr{};
@@ -1443,13 +1463,14 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   cudaError_t e;
   if (use_tc(h, T)) {
     n_ssum *= 4;
+    p.ssum_pitch = n_ssum;
     const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, c.wb, c.stream);
     if (rc != ARCHEAD_OK) return rc;
   } else {
     float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
     const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
     if (rc != ARCHEAD_OK) return rc;
-    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0};
+    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0, p.ssum_pitch};
     e = launch_after(g_kernel, dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream, gp);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
@@ -1534,7 +1555,7 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
     p.pitch = o.pitch;
     p.V = L.V;
     p.ssum = reinterpret_cast<float*>(wb + o.ssum);
-    p.tokens = nt;
+    p.ssum_pitch = static_cast<int32_t>(round_up(o.n_ssum, 4));   // 16-byte rows
     p.dx = reinterpret_cast<float*>(wb + o.dx);
     p.Kc = tc_kc(L);
     p.split_stride = static_cast<size_t>(nt) * p.Kc;

@@ -587,7 +587,7 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
           for (int r8 = 0; r8 < 4; ++r8)
             dst[32 * r8] = make_uint4(pack_half2(y[8 * r8], y[8 * r8 + 1]), pack_half2(y[8 * r8 + 2], y[8 * r8 + 3]),
                                       pack_half2(y[8 * r8 + 4], y[8 * r8 + 5]), pack_half2(y[8 * r8 + 6], y[8 * r8 + 7]));
-          if (col < ncol) p.ssum[(static_cast<size_t>(mt) * 4 + q) * p.T + col] = sum * (1.f / (1 << kTcGradScale));
+          if (col < ncol) p.ssum[(static_cast<size_t>(col) * p.n_mt128 + mt) * 4 + q] = sum * (1.f / (1 << kTcGradScale));
         } else if (col < ncol && nrow > 0) {
           const int t = tb + col;
           const float inv = __ldg(p.cinv + t);
