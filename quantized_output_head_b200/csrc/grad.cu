@@ -192,9 +192,9 @@ __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p
 
 // The h columns of X, and 2^-c_t, where the activation kernel is not used (many
 // tokens; heads with g_B not a multiple of 64, which it does not take); the z
-// columns come from a product with the fp16 rows of R and B (1769 x 2176 with 512 + 512 rows, g_B = 32, 2708
-// tokens: 0.16 ms for the whole gradient; with the decode path's z kernel, 8
-// tokens a pass over R and B, 2.4).  One block per token.
+// columns come from a product with the fp16 rows of R and B (1769 x 2176 with
+// 512 + 512 rows, g_B = 32, 2708 tokens: 0.16 ms for the whole gradient; with the
+// decode path's z kernel, 8 tokens a pass over R and B, 2.4).  One block per token.
 struct XParams {
   const uint16_t* hidden;
   uint16_t* xop;
