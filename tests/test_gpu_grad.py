@@ -262,3 +262,63 @@ def test_refusals(qoh):
         c.head.grad_hidden(h[:0], t[:0], lse[:0], g[:0])
     with pytest.raises(qoh.ArcheadError):
         c.head.grad_hidden(*c.args, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("shape", [SHAPES[0], SHAPES[4], SHAPES[5]])
+def test_many_tokens(qoh, shape):
+    """From 1024 tokens on z comes from fp16 rows of R and B: their rounding reaches the logits as well, by at most
+    2^-11 of sum |h| |R| |L| per logit, which is added to the forward's tolerance (two branches, on both sides of the
+    normalisation)."""
+    c = Case(qoh, shape, 1030, seed=90)
+    comps = c.comps
+
+    def real(codes, scales, group=None):
+        s = scales.view(np.float16).astype(np.float64)
+        return np.abs(codes * (s[:, None] if group is None else np.repeat(s, group, axis=1)))
+
+    low = real(comps["L"], comps["s_L"]) @ real(comps["R"], comps["s_R"])
+    low += real(comps["A"], comps["s_A"]) @ real(comps["B"], comps["s_B"], shape[5])
+    dz = 2.0 ** -11 * (np.abs(c.h) @ low.T)                  # [T, V]
+    dh, bound = c.expected()
+    p = np.exp(c.y - c.lse[:, None])
+    bound = bound + np.abs(c.g)[:, None] * ((p * np.expm1(2 * dz.max(axis=1))[:, None]) @ c.absW)
+    got = c.head.grad_hidden(*c.args).double().cpu().numpy()
+    bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(dh) + 1e-30
+    assert not got[c.g == 0].any()
+    assert np.all(np.abs(got - dh) <= bound), (np.abs(got - dh) / bound).max()
+
+
+@pytest.mark.parametrize("shape,T", [(SHAPES[0], 1100), (SHAPES[5], 300), (SHAPES[6], 300)])
+def test_many_tokens_without_a_gradient_hold_anything(qoh, shape, T):
+    c = Case(qoh, shape, T, seed=95)
+    hidden, targets, lse, _ = c.args
+    g = torch.where(torch.arange(T, device="cuda") % 3 == 1, 0.0, 1.0)
+    want = c.head.grad_hidden(hidden, targets, lse, g)
+    hidden, targets, lse = hidden.clone(), targets.clone(), lse.clone()
+    hidden[1::3], targets[1::3], lse[1::3] = NAN, -100, NAN
+    hidden[4] = float("inf")
+    ws = torch.full((c.head.grad_workspace_bytes(T),), 255, dtype=torch.uint8, device="cuda")
+    got = c.head.grad_hidden(hidden, targets, lse, g, workspace=ws)
+    assert torch.equal(got, want) and not got[1::3].any()
+    assert c.head.status(ws) == 0
+
+
+def test_chunks_and_passes_together(qoh):
+    """Two passes over the tokens of a head of two chunks of rows, against each token alone in a small call."""
+    shape, T = (70001, 128, 64, 16, 64, 64), 4096 + 300
+    comps = gen.random_components(gen.HeadShape(*shape), 97)
+    head = qoh.PackedHead(*shape, comps)
+    rnd = torch.Generator(device="cuda").manual_seed(98)
+    h = torch.randn(T, shape[1], generator=rnd, device="cuda").bfloat16()
+    targets = torch.randint(0, shape[0], (T,), generator=rnd, device="cuda", dtype=torch.int32)
+    targets[-1] = shape[0] - 1
+    grad = torch.randn(T, generator=rnd, device="cuda")
+    lse = torch.cat([head.lse_argmax(h[i:i + 512])[0] for i in range(0, T, 512)])
+    got = head.grad_hidden(h, targets, lse, grad, out_dtype=torch.float32).double()
+    for i in (0, 100, 4000, 4095, 4096, T - 100):
+        few = head.grad_hidden(h[i:i + 100], targets[i:i + 100].contiguous(), lse[i:i + 100].contiguous(),
+                               grad[i:i + 100].contiguous(), out_dtype=torch.float32).double()
+        part = got[i:i + 100]
+        # independent fp16 roundings on both sides (at most 4 * 2^-11, each)
+        rel = (part - few).norm(dim=1) / few.norm(dim=1)
+        assert float(rel.max()) <= 8 * 2.0 ** -11, (i, float(rel.max()))
