@@ -537,7 +537,8 @@ def policy_loss(ce: torch.Tensor, ce_old: torch.Tensor, advantages: torch.Tensor
         _check(_lib.archead_policy_loss(ce.data_ptr(), ce_old.data_ptr(), advantages.data_ptr(), _ptr(ce_ref), _ptr(mask),
                                         _ptr(cu_seqlens), T, S, ctypes.byref(opts), at, grad.data_ptr(), at + 4,
                                         ws.data_ptr(), 4 * ws.shape[0], stream), "archead_policy_loss")
-    return few[0], grad, few[1:]
+    # (as_strided takes half the time of indexing)
+    return few.as_strided((), ()), grad, few.as_strided((3,), (1,), 1)
 
 
 def preference_loss(ce: torch.Tensor, cu_seqlens: torch.Tensor, *, mask: Optional[torch.Tensor] = None,
@@ -571,7 +572,7 @@ def preference_loss(ce: torch.Tensor, cu_seqlens: torch.Tensor, *, mask: Optiona
         _check(_lib.archead_preference_loss(ce.data_ptr(), _ptr(ce_ref), _ptr(mask), cu_seqlens.data_ptr(), T, S // 2,
                                             ctypes.byref(opts), at, grad.data_ptr(), at + 4, ws.data_ptr(), 4 * ws.shape[0],
                                             stream), "archead_preference_loss")
-    return few[0], grad, few[1:].view(2, S // 2)
+    return few.as_strided((), ()), grad, few.as_strided((2, S // 2), (S // 2, 1), 1)
 
 
 def _loss_workspace(S) -> int:
@@ -629,7 +630,9 @@ def _check_mask(mask, T, device) -> torch.Tensor:
 def _check_cu(cu_seqlens, device):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.dtype not in (torch.int32, torch.int64):
         raise ValueError("cu_seqlens must be a one-dimensional int32 tensor of one offset more than sequences")
-    return cu_seqlens.to(device=device, dtype=torch.int32).contiguous(), cu_seqlens.shape[0] - 1
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.device != device:
+        cu_seqlens = cu_seqlens.to(device=device, dtype=torch.int32)
+    return cu_seqlens.contiguous(), cu_seqlens.shape[0] - 1
 
 
 def _check_hidden(hidden: torch.Tensor, d: int) -> None:

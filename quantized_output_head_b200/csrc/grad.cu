@@ -26,6 +26,8 @@
 //   4. dx_kernel             dX / S + (1/S - 1) W~[target], its low-rank
 //      columns to fp16; lowrank_rows_kernel: [s_R R | s_B B], fp16
 //   5. gemm finish           dh from dX_res + dz [s_R R | s_B B].
+// Few tokens: G from the forward kernels, gw_kernel for G W~, then 4 and 5; up to
+// 8 tokens finish_few_kernel in place of 5.
 //
 // Roundings to fp16: W~ entries (2^-11 relative, as in the forward), G (2^-11,
 // stored times 2^15 so that a probability keeps its full precision down to
@@ -1228,6 +1230,122 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
   }
 }
 
+// dh of up to kDecodeTokens tokens from dX_res + dz [s_R R | s_B B], the int8
+// codes as they are.  A block owns 64 columns; 32 half warps take every 32nd row,
+// 8 rows in flight, the first ones before the wait (they are weights), and their
+// sums meet in shared memory in a fixed order.  The tensor-core product's set-up
+// and its fp16 rows of R and B are most of its time here: the whole gradient of
+// one token of 32003 x 2048 took 70.7 us with it, 64.8 so; of 8000 x 512 45.2 and
+// 38.4; 8 tokens of 8000 x 512 55.5 and 50.6.
+struct FinishFewParams {
+  const int8_t* R;
+  const uint16_t* s_R;
+  const int8_t* B;
+  const uint16_t* s_B;
+  const uint16_t* dz;         // [T][Kz], operand order
+  const float* dx;            // [T][Kc], operand order
+  const float* grad;
+  const int32_t* targets;
+  void* out;
+  uint32_t* status;
+  int32_t T, d, Kc, Kz, rcp, rrp, g_B, v_total, out_f32;
+  float mul_c, mul_r, mul_dx;
+};
+constexpr int kFinishChunk = 512, kFinishRows = 8;   // dz columns in shared memory; rows in flight
+
+// Four columns of the low-rank row at position e of the operand order.
+__device__ __forceinline__ float4 lowrank_row4(const FinishFewParams& p, int e, int j) {
+  const int k = (e & ~15) + tc_kcol(e & 15);
+  const bool core = k < p.rcp;
+  const int r = core ? k : k - p.rcp;
+  if (e >= p.Kz || (!core && r >= p.rrp)) return make_float4(0.f, 0.f, 0.f, 0.f);
+  const char4 c = __ldg(reinterpret_cast<const char4*>((core ? p.R : p.B) + static_cast<size_t>(r) * p.d + j));
+  float4 s;
+  if (core) {
+    s.x = s.y = s.z = s.w = __half2float(__ushort_as_half(__ldg(p.s_R + r))) * p.mul_c;
+  } else {
+    const uint16_t* sb = p.s_B + static_cast<size_t>(r) * (p.d / p.g_B);
+    const auto at = [&](int col) { return __half2float(__ushort_as_half(__ldg(sb + col / p.g_B))) * p.mul_r; };
+    s.x = at(j);
+    s.y = s.z = s.w = s.x;
+    if (p.g_B % 4 != 0) {
+      s.y = at(j + 1);
+      s.z = at(j + 2);
+      s.w = at(j + 3);
+    }
+  }
+  return make_float4(c.x * s.x, c.y * s.y, c.z * s.z, c.w * s.w);
+}
+
+template <int TT>
+__global__ void __launch_bounds__(512) finish_few_kernel(const FinishFewParams p) {
+  __shared__ __align__(16) float sh[16 * TT * 64];     // dz of a chunk, then the warps' sums
+  static_assert(kFinishChunk <= 16 * 64, "dz of a chunk fits");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slot = threadIdx.x >> 4;
+  const int j0 = blockIdx.x * 64, j = j0 + 4 * (lane & 15);
+  // this thread's result: token t, column j0 + col
+  const int t = threadIdx.x >> 6, col = threadIdx.x & 63;
+  const bool mine = t < TT && t < p.T;
+  const float g = mine ? p.grad[t] : 0.f;
+  const int target = mine ? p.targets[t] : -1;
+  float4 w[kFinishRows], next[kFinishRows];
+#pragma unroll
+  for (int i = 0; i < kFinishRows; ++i) w[i] = lowrank_row4(p, slot + 32 * i, j);
+  grid_dependency_wait();
+  const float res = mine ? p.dx[static_cast<size_t>(t) * p.Kc + j0 + (col & ~15) + tc_kpos(col & 15)] : 0.f;
+  float acc[TT][4] = {};
+  for (int c0 = 0; c0 < p.Kz; c0 += kFinishChunk) {
+    const int n = min(kFinishChunk, p.Kz - c0);
+    if (c0 > 0) __syncthreads();
+#pragma unroll
+    for (int tt = 0; tt < TT; ++tt)
+      for (int e = threadIdx.x; e < n; e += 512)
+        sh[e * TT + tt] = tt < p.T ? __half2float(__ushort_as_half(p.dz[static_cast<size_t>(tt) * p.Kz + c0 + e])) : 0.f;
+    __syncthreads();
+    for (int b = 0; b < n; b += 32 * kFinishRows) {
+#pragma unroll
+      for (int i = 0; i < kFinishRows; ++i) next[i] = lowrank_row4(p, c0 + b + slot + 32 * (kFinishRows + i), j);
+#pragma unroll
+      for (int i = 0; i < kFinishRows; ++i) {
+        const int e = b + slot + 32 * i;
+        if (e < n) {
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt) {
+            const float z = sh[e * TT + tt];
+            acc[tt][0] = fmaf(z, w[i].x, acc[tt][0]);
+            acc[tt][1] = fmaf(z, w[i].y, acc[tt][1]);
+            acc[tt][2] = fmaf(z, w[i].z, acc[tt][2]);
+            acc[tt][3] = fmaf(z, w[i].w, acc[tt][3]);
+          }
+        }
+        w[i] = next[i];
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[tt][c] += __shfl_xor_sync(0xffffffffu, acc[tt][c], 16);
+    if (lane < 16)
+      *reinterpret_cast<float4*>(sh + (warp * TT + tt) * 64 + 4 * lane) =
+          make_float4(acc[tt][0], acc[tt][1], acc[tt][2], acc[tt][3]);
+  }
+  __syncthreads();
+  if (!mine) return;
+  float x = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x += sh[(i * TT + t) * 64 + col];
+  x = g == 0.f ? 0.f : fmaf(res, p.mul_dx, x) * g;
+  if (g != 0.f && (target < 0 || target >= p.v_total)) {
+    x = grad_nan();
+    if (j0 + col == 0) atomicOr(p.status, static_cast<uint32_t>(ARCHEAD_STATUS_BAD_TARGET));
+  }
+  const size_t at = static_cast<size_t>(t) * p.d + j0 + col;
+  if (p.out_f32) static_cast<float*>(p.out)[at] = x;
+  else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(x);
+}
+
 // -------------------------------------------------------------------- host
 // Few tokens: the packed rows are dequantised inside the second product,
 // kFewPass tokens a pass over the head.  One such pass beats the chunks of W~ at
@@ -1291,7 +1409,8 @@ int accumulate_splits(int tokens, int Kc, int chunk, int pairs) {
 }
 
 struct GradLayout {
-  bool few, own_x;                 // own_x: X by x_hidden_kernel and a product
+  bool few, direct;                // direct: so few that the last product takes R and B as they are
+  bool own_x;                      // X by x_hidden_kernel and a product
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
   int pitch, n_ssum;
   size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, rbp, total;
@@ -1314,6 +1433,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
   const int passes = (T + kFewPass - 1) / kFewPass;
   const size_t t = o.few ? (T + passes - 1) / passes : std::min(T, kGradTokens);
   o.tokens = static_cast<int>(t);
+  o.direct = t <= kDecodeTokens;
   if (o.few) {
     // The forward call's workspace comes first: its header is this one's.
     o.fwd = ws_layout(h, o.tokens).total;
@@ -1337,7 +1457,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
   o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
-  o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
+  if (!o.direct) o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
   if (o.own_x) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 2);
   o.total = at;
   return o;
@@ -1414,7 +1534,7 @@ cudaError_t grad_activations(const GradCall& c, const uint16_t* hidden, GemmPara
 // tickets of the activation kernel).
 int grad_lowrank(const GradCall& c) {
   const Layout& L = c.h.L;
-  if (c.o.Kz == 0) {
+  if (c.o.Kz == 0 || c.o.direct) {
     const cudaError_t e = cudaMemsetAsync(c.wb, 0, 256, c.stream);
     return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
   }
@@ -1439,6 +1559,19 @@ int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const 
   DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
   cudaError_t e = launch_after(dx_kernel, dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream, dp);
+  if (e == cudaSuccess && c.o.direct) {
+    const FinishFewParams f{reinterpret_cast<const int8_t*>(c.h.arena + L.off_R),
+                            reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sR),
+                            reinterpret_cast<const int8_t*>(c.h.arena + L.off_B),
+                            reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sB),
+                            dz, p.dx, p.grad, p.targets, p.out, p.status, nt, L.d, Kc, Kz, L.rcp, L.rrp, L.g_B, p.v_total,
+                            p.out_f32, std::ldexp(1.f, -c.h.tc_beta), std::ldexp(1.f, -c.h.tc_gamma),
+                            std::ldexp(1.f, -kGradScale - c.h.tc_alpha)};
+    const auto kernel = nt == 1 ? finish_few_kernel<1> : nt == 2 ? finish_few_kernel<2>
+                        : nt <= 4 ? finish_few_kernel<4> : finish_few_kernel<8>;
+    e = launch_after(kernel, dim3(L.d / 64), 512, 0, c.stream, f);
+    return e == cudaSuccess ? ARCHEAD_OK : set_cuda_error(e);
+  }
   CUtensorMap mz{}, mr{};
   if (e == cudaSuccess && Kz > 0) {
     e = tc_encode_map(&mz, dz, Kz, nt, Kz, kGM / 2);
