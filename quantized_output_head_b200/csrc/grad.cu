@@ -1035,7 +1035,8 @@ __global__ void __launch_bounds__(kGwWarps * 32, 1) gw_kernel(const GwParams p) 
     const int gr = lane >> 2, cc = lane & 3;
     // byte offsets of this lane inside a tile: row 16 j + gr, 16-byte pieces 2 cc and 2 cc + 1 (swizzled by the row)
     const uint32_t row = tiles + static_cast<uint32_t>((16 * j + gr) * 128);
-    const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16), o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
+    const uint32_t o_lo = row + static_cast<uint32_t>(((2 * cc) ^ gr) * 16);
+    const uint32_t o_hi = row + static_cast<uint32_t>(((2 * cc + 1) ^ gr) * 16);
 
     // The next tile's packed bytes, two pairs of chunks.  Every load has its own
     // register and at most a predicate: a load under a branch that others share a
@@ -1619,7 +1620,8 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   w.dx = p.dx;
   w.split_stride = p.split_stride;
   w.status = p.status;
-  const auto kernel = w.rows.g_log2 >= 7 ? gw_kernel<1> : w.rows.g_log2 == 6 ? gw_kernel<2> : w.rows.g_log2 == 5 ? gw_kernel<4> : gw_kernel<8>;
+  const int gl = w.rows.g_log2;
+  const auto kernel = gl >= 7 ? gw_kernel<1> : gl == 6 ? gw_kernel<2> : gl == 5 ? gw_kernel<4> : gw_kernel<8>;
   e = launch_after(kernel, dim3(g.grid), kGwWarps * 32, kGwSmem, c.stream, w);
   if (e != cudaSuccess) return set_cuda_error(e);
   return grad_finish(c, p, n_ssum, 0, g.s);
@@ -1692,7 +1694,7 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
     p.dx = reinterpret_cast<float*>(wb + o.dx);
     p.Kc = tc_kc(L);
     p.split_stride = static_cast<size_t>(nt) * p.Kc;
-    p.out = out_f32 ? static_cast<void*>(static_cast<float*>(out) + first) : static_cast<void*>(static_cast<uint16_t*>(out) + first);
+    p.out = static_cast<uint8_t*>(out) + first * (out_f32 ? 4 : 2);
     p.out_f32 = out_f32 ? 1 : 0;
     rc = o.few ? grad_few(c, hidden + first, p) : grad_many(c, hidden + first, p);
   }

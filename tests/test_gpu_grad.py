@@ -322,3 +322,12 @@ def test_chunks_and_passes_together(qoh):
         # independent fp16 roundings on both sides (at most 4 * 2^-11, each)
         rel = (part - few).norm(dim=1) / few.norm(dim=1)
         assert float(rel.max()) <= 8 * 2.0 ** -11, (i, float(rel.max()))
+
+
+@pytest.mark.parametrize("shape", [(700, 640, 600, 70, 64, 64), (700, 640, 400, 700, 64, 20)])
+@pytest.mark.parametrize("T", [1, 3, 4, 7])
+def test_few_tokens_of_many_low_rank_rows(qoh, shape, T):
+    """More low-rank rows than the last product of a few tokens keeps in shared memory at a time."""
+    c = Case(qoh, shape, T, seed=100 + T)
+    c.check(c.head.grad_hidden(*c.args), 2.0 ** -8)
+    c.check(c.head.grad_hidden(*c.args, out_dtype=torch.float32), 2.0 ** -24)
