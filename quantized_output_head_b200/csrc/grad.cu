@@ -270,7 +270,7 @@ __host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) 
   return block < g.res ? g.s_res : block + 1 < g.res + g.rest ? g.s_rest : g.s_last;
 }
 
-// Blocks of 1024 columns per token: S from the tiles' partial sums (in a fixed
+// Blocks of 1024 (or 256) columns per token: S from the tiles' partial sums (in a fixed
 // order), then dX (added over the K splits) / S + (1/S - 1) W~[target]; the
 // residual columns stay fp32 in the first split's place, the low-rank ones become
 // the fp16 operand dz [T][Kz'].  Latency is all there is to it at few tokens: the
@@ -288,32 +288,48 @@ struct DxParams {
   int32_t splits;                                  // partial dX of every column, or (0) by
   GwSplits gw;
 };
+// Up to kDxWaysTokens tokens the partial dX of a column are added by 4 threads
+// (whole gradient: 16 tokens of 8000 x 512 41.1 us with one, 37.6 with 4; 64 tokens
+// of 65531 x 1024 69.3 and 66.2, of 32003 x 2048 81.6 and 80.4; but 128 tokens of
+// 32003 x 2048 100.6 and 103, each block adding up S anew).
+constexpr int kDxWays = 4, kDxWaysTokens = 64;
+template <int kWays>
 __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
+  constexpr int kCols = 256 / kWays;                  // float4 columns of a block
   __shared__ float part[8];
+  __shared__ float4 sums[kWays > 1 ? 256 : 1];
   // What the call was given may be read before the wait: the call's first kernel
   // is not a dependent launch.
   const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q = blockIdx.y * 256 + threadIdx.x;
-  const bool in = q < p.Kc / 4, live = p.grad[t] != 0.f;   // (else its row of dX is zero, S has no meaning)
+  const int way = threadIdx.x / kCols, q = blockIdx.y * kCols + threadIdx.x % kCols;
+  const bool in = q < p.Kc / 4, out = in && way == 0, live = p.grad[t] != 0.f;   // (else its row of dX is zero, S has no meaning)
   const int target = p.whole && live ? p.targets[t] - p.row0 : -1;
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (in && target >= 0 && target < p.V)
+  if (out && target >= 0 && target < p.V)
     w = packed_row4(p.rows, p.rows.mtiles + static_cast<size_t>(target / kMT) * p.rows.mblk_bytes, target % kMT, q);
   grid_dependency_wait();
   grid_launch_dependents();
   float4* dx = reinterpret_cast<float4*>(p.dx + static_cast<size_t>(t) * p.Kc) + q;
   uint2* dz = reinterpret_cast<uint2*>(p.dz + static_cast<size_t>(t) * (p.Kc - p.d) + 4 * q - p.d);
   if (!live) {
-    if (in && 4 * q >= p.d) *dz = make_uint2(0u, 0u);
+    if (out && 4 * q >= p.d) *dz = make_uint2(0u, 0u);
     return;
   }
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (in) {
-    v = *dx;
     const int n = p.splits > 0 ? p.splits : gw_splits(p.gw, 4 * q / kGwCols);
 #pragma unroll 8
-    for (int s = 1; s < n; ++s) {
+    for (int s = way; s < n; s += kWays) {
       const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(dx) + s * p.split_stride);
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+  }
+  if constexpr (kWays > 1) {
+    sums[threadIdx.x] = v;
+    __syncthreads();
+#pragma unroll
+    for (int i = 1; i < kWays; ++i) {
+      const float4 x = sums[i * kCols + threadIdx.x % kCols];
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
   }
@@ -336,7 +352,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
     for (int i = 0; i < 8; ++i) s += part[i];
     r = 1.f / s;
   }
-  if (!in) return;
+  if (!out) return;
   const float c = (r - 1.f) * static_cast<float>(1 << kGradScale);
   v = make_float4(fmaf(c, w.x, v.x * r), fmaf(c, w.y, v.y * r), fmaf(c, w.z, v.z * r), fmaf(c, w.w, v.w * r));
   if (4 * q < p.d) {
@@ -1559,7 +1575,10 @@ int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const 
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
   DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
-  cudaError_t e = launch_after(dx_kernel, dim3(nt, (Kc + 1023) / 1024), 256, 0, c.stream, dp);
+  const bool ways = nt <= kDxWaysTokens;
+  const auto dx = ways ? dx_kernel<kDxWays> : dx_kernel<1>;
+  const int cols = ways ? 1024 / kDxWays : 1024;
+  cudaError_t e = launch_after(dx, dim3(nt, (Kc + cols - 1) / cols), 256, 0, c.stream, dp);
   if (e == cudaSuccess && c.o.direct) {
     const FinishFewParams f{reinterpret_cast<const int8_t*>(c.h.arena + L.off_R),
                             reinterpret_cast<const uint16_t*>(c.h.arena + L.off_sR),
