@@ -331,3 +331,29 @@ def test_few_tokens_of_many_low_rank_rows(qoh, shape, T):
     c = Case(qoh, shape, T, seed=100 + T)
     c.check(c.head.grad_hidden(*c.args), 2.0 ** -8)
     c.check(c.head.grad_hidden(*c.args, out_dtype=torch.float32), 2.0 ** -24)
+
+
+def test_many_tokens_on_streams_and_in_graphs(qoh):
+    """Two calls of the many-token path at once, and each captured and replayed, with the bits of a call alone."""
+    a, b = Case(qoh, SHAPES[0], 1100, seed=110), Case(qoh, SHAPES[6], 300, seed=111)
+    want = [x.head.grad_hidden(*x.args) for x in (a, b)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(4):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            x = (a, b)[i % 2]
+            got.append(x.head.grad_hidden(*x.args))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))
+    graphs = []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = x.head.grad_hidden(*x.args)
+        graphs.append((g, out))
+    a.args[3].mul_(2.0)
+    for _ in range(2):
+        for g, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(graphs[0][1], want[0] * 2) and torch.equal(graphs[1][1], want[1])
