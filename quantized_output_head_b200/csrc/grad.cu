@@ -3,20 +3,25 @@
 //
 // With y[t] = W h[t] over all rows of the head, lse[t] its log-sum-exp and
 // g[t] = dLoss / dce[t], ce[t] = lse[t] - y[t, target[t]]:
-//   G[t,v]  = exp(y[t,v] - lse[t]) - [v = target[t]]
-//   dh[t,:] = g[t] sum_v G[t,v] W[v,:].
+//   dh[t,:] = g[t] sum_v (p[t,v] - [v = target[t]]) W[v,:],   p = exp(y - lse).
 // W is never formed.  With W~ the concatenated packed operand of the
 // tensor-core forward (tc_params.h; columns residual | core | correction)
-//   y = 2^-c_t X W~^T,        dX = G W~   (one row of d + r_c' + r_r' columns),
+//   y = 2^-c_t X W~^T,        G = p, but 0 at the target's row,
+//   dX = G W~ + (p[target] - 1) W~[target]   (one row of d + r_c' + r_r' columns),
 //   dh = g ( dX_res + dX_core (s_R R) + dX_corr (s_B B) ),
 // so the low-rank factors are applied once per token, not once per row.
 //
 // The recomputed logits carry the forward's rounding (up to ~1e-2 where y is
 // large), the given lse that of whichever kernel made it; a row that holds most
 // of the mass would get all of their difference.  So the probabilities are
-// normalised by their own sum S[t] = sum_v exp(y[t,v] - lse[t]), after the fact:
-//   sum_v (exp(y - lse) / S - [v = target]) W[v] = (G W) / S + (1/S - 1) W[target].
-// (On a vocabulary shard S is not known and lse is taken as it is.)
+// normalised by their own sum S[t] = Rest[t] + p[t,target], Rest[t] = sum_v G[t,v],
+// after the fact:
+//   sum_v (p / S - [v = target]) W[v] = (G W) / S - (Rest / S) W[target].
+// No term cancels: with the target's p - 1 inside G, its coefficient 1 - p of a
+// confident token would be a difference of terms of size |S - 1| that are rounded
+// to fp16 (rows of 1 - p = 1e-5 were 45 % off with lse off by 1e-2).
+// (On a vocabulary shard S is not known: lse is taken as it is, the coefficient
+// is p - 1.)
 //
 // Many tokens: the vocabulary is walked in chunks of rows.  Per chunk
 //   1. dequant_rows_kernel   W~ of the chunk, fp16, in the workspace
@@ -270,8 +275,8 @@ __host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) 
   return block < g.res ? g.s_res : block + 1 < g.res + g.rest ? g.s_rest : g.s_last;
 }
 
-// Blocks of 1024 (or 256) columns per token: S from the tiles' partial sums (in a fixed
-// order), then dX (added over the K splits) / S + (1/S - 1) W~[target]; the
+// Blocks of 1024 (or 256) columns per token: Rest from the tiles' partial sums (in a
+// fixed order), then dX (added over the K splits) / S - (Rest / S) W~[target]; the
 // residual columns stay fp32 in the first split's place, the low-rank ones become
 // the fp16 operand dz [T][Kz'].  Latency is all there is to it at few tokens: the
 // loads are issued in batches, a token's partial sums lie side by side, and the
@@ -279,6 +284,7 @@ __host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) 
 struct DxParams {
   DequantParams rows;
   const float* ssum;          // [tokens][ssum_pitch], n_ssum of them used
+  const float* ptgt;          // [tokens]
   const float* grad;
   const int32_t* targets;
   float* dx;
@@ -303,9 +309,10 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
   const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int way = threadIdx.x / kCols, q = blockIdx.y * kCols + threadIdx.x % kCols;
   const bool in = q < p.Kc / 4, out = in && way == 0, live = p.grad[t] != 0.f;   // (else its row of dX is zero, S has no meaning)
-  const int target = p.whole && live ? p.targets[t] - p.row0 : -1;
+  const int target = live ? p.targets[t] - p.row0 : -1;
+  const bool here = target >= 0 && target < p.V;   // (of these rows)
   float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (out && target >= 0 && target < p.V)
+  if (out && here)
     w = packed_row4(p.rows, p.rows.mtiles + static_cast<size_t>(target / kMT) * p.rows.mblk_bytes, target % kMT, q);
   grid_dependency_wait();
   grid_launch_dependents();
@@ -333,7 +340,8 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
   }
-  float r = 1.f;
+  const float own = here ? p.ptgt[t] : 0.f;
+  float r = 1.f, c = own - 1.f;
   if (p.whole) {
     const float* parts = p.ssum + static_cast<size_t>(t) * p.ssum_pitch;
     float s = 0.f;
@@ -350,10 +358,11 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += part[i];
-    r = 1.f / s;
+    r = 1.f / (s + own);
+    c = -s * r;
   }
   if (!out) return;
-  const float c = (r - 1.f) * static_cast<float>(1 << kGradScale);
+  c *= static_cast<float>(1 << kGradScale);
   v = make_float4(fmaf(c, w.x, v.x * r), fmaf(c, w.y, v.y * r), fmaf(c, w.z, v.z * r), fmaf(c, w.w, v.w * r));
   if (4 * q < p.d) {
     *dx = v;
@@ -416,8 +425,9 @@ struct GemmParams {
   const float* lse;                    // [M]
   uint16_t* G;                         // [M][pitch]
   int32_t pitch, v0, V;                // first row of the chunk, rows of the head
-  float* ssum;                         // [tokens][ssum_pitch]: sums of exp(y - lse) over half a tile's rows
+  float* ssum;                         // [tokens][ssum_pitch]: sums of G over half a tile's rows
   int32_t ssum_pitch;
+  float* ptgt;                         // [tokens]: exp(y - lse) of the target's row
   uint16_t* x;                         // lowrank: z columns of X, [M][Kc]
   // accumulate / finish
   float* dx;                           // [splits][M][Kc]
@@ -647,13 +657,19 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
             for (int c = 0; c < 32; ++c)
               if (c >= left) x[c] = 0.f;
           }
-#pragma unroll
-          for (int c = 0; c < 32; c += 4) ssum += (x[c] + x[c + 1]) + (x[c + 2] + x[c + 3]);
-          if (__any_sync(0xffffffffu, g != 0.f && tl >= 0 && tl < 32)) {
+          const bool own = g != 0.f && tl >= 0 && tl < 32;
+          if (__any_sync(0xffffffffu, own)) {
+            float pt = 0.f;
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (g != 0.f && c == tl) x[c] -= static_cast<float>(1 << kGradScale);
+              if (c == tl) {
+                pt = x[c];
+                x[c] = 0.f;
+              }
+            if (own) p.ptgt[t] = pt * (1.f / (1 << kGradScale));
           }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) ssum += (x[c] + x[c + 1]) + (x[c + 2] + x[c + 3]);
 #pragma unroll
           for (int c = 0; c < 32; c += 2) tile[lane * 17 + c / 2] = pack_half2(x[c], x[c + 1]);
           __syncwarp();
@@ -825,7 +841,8 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
 // of 8 rows, the 32 tokens of a run side by side, so that a warp's load of one
 // run per lane (= token) is 512 contiguous bytes.  (Read row by row, 16 bytes of
 // 32 rows per load, G cost gw_kernel 37 of 161 us at 64 tokens.)  One block per
-// piece, with its tokens' sums of exp(y - lse).
+// piece, with its tokens' sums of G and, where the target is one of the rows, its
+// exp(y - lse).
 struct GParams {
   const float* y;
   const float* lse;
@@ -833,6 +850,7 @@ struct GParams {
   const int32_t* targets;
   uint4* G;                   // [k-step][T / 32][16][32]
   float* ssum;                // [T][ssum_pitch], one per k-step
+  float* ptgt;                // [T]
   int32_t T, V, row0, ssum_pitch;
 };
 constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
@@ -853,8 +871,11 @@ __global__ void __launch_bounds__(256) g_kernel(const GParams p) {
     for (int e = 0; e < kGwRows / 32; ++e) {
       const int v = v0 + 32 * e + lane;
       float x = live && v < p.V ? __expf(y[v] - lse) : 0.f;
+      if (live && v == target) {
+        if (v < p.V) p.ptgt[t] = x;
+        x = 0.f;
+      }
       sum += x;
-      if (live && v == target) x -= 1.f;
       piece[4 * e + (lane >> 3)][tl][lane & 7] = __half_as_ushort(__float2half_rn(x * static_cast<float>(1 << kGradScale)));
     }
 #pragma unroll
@@ -1430,7 +1451,7 @@ struct GradLayout {
   bool own_x;                      // X by x_hidden_kernel and a product
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
   int pitch, n_ssum;
-  size_t fwd, logits, cinv, ssum, xop, w, g, dx, dz, rb, rbp, total;
+  size_t fwd, logits, cinv, ssum, ptgt, xop, w, g, dx, dz, rb, rbp, total;
 };
 
 GradLayout grad_layout(const archead_handle& h, int T) {
@@ -1471,6 +1492,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
   }
   o.ssum = take(t * (o.few ? 4 * o.n_ssum : round_up(o.n_ssum, 4)) * 4);
+  o.ptgt = take(t * 4);
   o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
@@ -1573,7 +1595,7 @@ int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const 
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
-  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
+  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.ptgt, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
   const bool ways = nt <= kDxWaysTokens;
   const auto dx = ways ? dx_kernel<kDxWays> : dx_kernel<1>;
@@ -1617,13 +1639,13 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   if (use_tc(h, T)) {
     n_ssum *= 4;
     p.ssum_pitch = n_ssum;
-    const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, c.wb, c.stream);
+    const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, p.ptgt, c.wb, c.stream);
     if (rc != ARCHEAD_OK) return rc;
   } else {
     float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
     const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
     if (rc != ARCHEAD_OK) return rc;
-    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, T, L.V, h.row0, p.ssum_pitch};
+    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, p.ptgt, T, L.V, h.row0, p.ssum_pitch};
     e = launch_after(g_kernel, dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream, gp);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
@@ -1710,6 +1732,7 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
     p.V = L.V;
     p.ssum = reinterpret_cast<float*>(wb + o.ssum);
     p.ssum_pitch = static_cast<int32_t>(round_up(o.n_ssum, 4));   // 16-byte rows
+    p.ptgt = reinterpret_cast<float*>(wb + o.ptgt);
     p.dx = reinterpret_cast<float*>(wb + o.dx);
     p.Kc = tc_kc(L);
     p.split_stride = static_cast<size_t>(nt) * p.Kc;

@@ -152,9 +152,10 @@ cudaError_t launch_shard_merge(const float4* parts, int n, int T, float* lse, in
 int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float* logits, void* ws, size_t ws_bytes,
                    cudaStream_t stream);
 
-// The tensor-core kernel's gradient instance (T <= kTcMaxBN, tc_ok): G and its sums in place of logits.
+// The tensor-core kernel's gradient instance (T <= kTcMaxBN, tc_ok): G, its sums and the targets' own
+// probabilities in place of logits.
 int forward_tc_grad(const archead_handle& h, const uint16_t* hidden, int T, const int32_t* targets, const float* lse,
-                    const float* grad, void* G, float* ssum, void* ws, cudaStream_t stream);
+                    const float* grad, void* G, float* ssum, float* ptgt, void* ws, cudaStream_t stream);
 
 // Gradient of the head (grad.cu).
 cudaError_t grad_set_attributes();

@@ -531,9 +531,10 @@ __device__ void mma_warp(const TcParams& p, const TcSmem& sm, uint32_t tmem_base
 // target logit if it falls in these rows, and the logits row segment if asked.
 // The four warps' states of a token are merged into one partial per
 // (token, 128-row tile).
-// kGrad: what goes out is the gradient's G = exp(y - lse) - [row = target], fp16
-// times 2^kTcGradScale, a lane's token and 8 rows in one 16-byte run (the runs of
-// 32 tokens side by side), and the sum of exp(y - lse) over the 32 rows.
+// kGrad: what goes out is the gradient's G = exp(y - lse), 0 at the target's row,
+// fp16 times 2^kTcGradScale, a lane's token and 8 rows in one 16-byte run (the
+// runs of 32 tokens side by side), its sum over the 32 rows, and the target's own
+// exp(y - lse) by itself.
 template <bool kGrad>
 __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tmem_base, int ew, int lane) {
   grid_dependency_wait();   // 2^-c_t, and the previous call's readers of the outputs
@@ -571,17 +572,22 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
           float y[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) y[k] = exp2_approx(fmaf(tile[lane * 33 + k], k2, -l2));
-          float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+          for (int k = 0; k < 32; ++k)
             if (!live || k >= nrow) y[k] = 0.f;
-            sum += y[k];
-          }
           if (__any_sync(0xffffffffu, tg >= 0 && tg < nrow)) {
+            float own = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (k == tg && k < nrow) y[k] -= static_cast<float>(1 << kTcGradScale);
+              if (k == tg) {
+                own = y[k];
+                y[k] = 0.f;
+              }
+            if (tg >= 0 && tg < nrow) p.ptgt[col] = own * (1.f / (1 << kTcGradScale));
           }
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) sum += y[k];
           uint4* dst = p.G + (static_cast<size_t>(mt) * ((p.T + 31) / 32) + c0 / 32) * (kTcBM / 8 * 32) + 4 * q * 32 + lane;
 #pragma unroll
           for (int r8 = 0; r8 < 4; ++r8)
