@@ -158,11 +158,15 @@ struct LowrankParams {
   const int8_t* B;
   const uint16_t* s_B;
   uint16_t* out;
-  uint16_t* out_perm;         // or null: the same rows, columns in the operand order (z of heads without act_prep)
+  uint16_t* out_perm;         // or null: [Kz'][2 d], columns in the operand order: the rows, then what fp16 left of them
   uint32_t* header;           // 64 words of the workspace: status, tickets
   int32_t d, rcp, rrp, Kz, g_B;
   float mul_c, mul_r;
 };
+// (For z a row is the sum of two fp16 ones: a code times an fp16 scale has at most 19
+// bits, so the pair is exact and z is that of the forward's activation kernel.  The
+// rounded rows alone move the logits by up to 2^-11 of their size, which a vocabulary
+// shard, whose probabilities nothing normalises, would carry into its gradient.)
 // A thread per 8 columns; the first block also clears the workspace header.
 __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p) {
   if (blockIdx.x == 0 && threadIdx.x < 64) p.header[threadIdx.x] = 0u;
@@ -171,7 +175,7 @@ __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p
   if (e >= p.Kz) return;
   const int k = (e & ~15) + tc_kcol(e & 15);
   const bool core = k < p.rcp;
-  uint32_t o[4] = {0u, 0u, 0u, 0u};
+  uint32_t o[4] = {0u, 0u, 0u, 0u}, left[4] = {0u, 0u, 0u, 0u};
   if (core || k - p.rcp < p.rrp) {
     const int r = core ? k : k - p.rcp;
     const uint2 codes = __ldg(reinterpret_cast<const uint2*>((core ? p.R : p.B) + static_cast<size_t>(r) * p.d + j));
@@ -187,20 +191,25 @@ __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p
         if (!core) v[h] *= __half2float(__ushort_as_half(sb[(j + c + h) / p.g_B]));
       }
       o[c / 2] = pack_half2(v[0], v[1]);
+      const float2 f = half2_bits_to_float2(o[c / 2]);
+      left[c / 2] = pack_half2(v[0] - f.x, v[1] - f.y);
     }
   }
   *reinterpret_cast<uint4*>(p.out + static_cast<size_t>(e) * p.d + j) = make_uint4(o[0], o[1], o[2], o[3]);
   if (p.out_perm != nullptr) {
+    uint16_t* row = p.out_perm + static_cast<size_t>(e) * 2 * p.d + (j & ~15);
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint32_t*>(p.out_perm + static_cast<size_t>(e) * p.d + (j & ~15) + tc_kpos((j & 15) + 2 * c)) = o[c];
+    for (int c = 0; c < 4; ++c) {
+      *reinterpret_cast<uint32_t*>(row + tc_kpos((j & 15) + 2 * c)) = o[c];
+      *reinterpret_cast<uint32_t*>(row + p.d + tc_kpos((j & 15) + 2 * c)) = left[c];
+    }
   }
 }
 
 // The h columns of X, and 2^-c_t, where the activation kernel is not used (many
 // tokens; heads with g_B not a multiple of 64, which it does not take); the z
-// columns come from a product with the fp16 rows of R and B (1769 x 2176 with
-// 512 + 512 rows, g_B = 32, 2708 tokens: 0.16 ms for the whole gradient; with the
+// columns come from a product with the rows of R and B as pairs of fp16 rows (1769 x 2176 with
+// 512 + 512 rows, g_B = 32, 2708 tokens: 0.18 ms for the whole gradient; with the
 // decode path's z kernel, 8 tokens a pass over R and B, 2.4).  One block per token.
 struct XParams {
   const uint16_t* hidden;
@@ -510,7 +519,9 @@ __device__ void g_tma_warp(const GemmParams& p, const GemmSmem& sm, const CUtens
         const uint32_t a = sm.stages + s * kGStageBytes, b = a + kGABytes;
         const uint32_t bar = cluster_addr(sm.full + 8 * s, 0);   // the leader's
         if (rank == 0) mbar_arrive_expect_tx(sm.full + 8 * s, bytes);
-        tma_load_2d_pair(a, ma, k * 64, w.m * kGM + rank * (kGM / 2), bar);
+        // (z: the same h times the rows, then times what fp16 left of them)
+        const int ka = kMode == kLowrank && k >= p.n_k / 2 ? k - p.n_k / 2 : k;
+        tma_load_2d_pair(a, ma, ka * 64, w.m * kGM + rank * (kGM / 2), bar);
         if constexpr (!gemm_b_mn(kMode)) {
           tma_load_2d_pair(b, mb, k * 64, n0, bar);
         } else {
@@ -1392,11 +1403,11 @@ __global__ void __launch_bounds__(512) finish_few_kernel(const FinishFewParams p
 // in one chunk, 65531 x 1024: 160 to 198 us against 142).
 constexpr int kFewPass = 128;
 
-// Many tokens of a head with low-rank rows: z by a product with the fp16 rows of
-// R and B from this many tokens on, below by the activation kernel, which has one
-// launch less (whole gradient, 151936 x 4096: 384 tokens 1741 against 1703 us,
-// 4096 tokens 9.74 against 9.88 ms; 32003 x 2048: 384 tokens 205 against 203 us,
-// 1024 324 against 333, 4096 1022 against 1117).
+// Many tokens of a head with low-rank rows: z by a product with the rows of R and B
+// (pairs of fp16 rows) from this many tokens on, below by the activation kernel,
+// which has one launch less (whole gradient, 151936 x 4096: 1024 tokens 2.94
+// against 2.97 ms, 4096 tokens 9.65 against 9.83 ms; 32003 x 2048: 1024 tokens 374
+// against 371 us, 4096 1179 against 1225).
 constexpr int kOwnXTokens = 1024;
 
 // Work split of gw_kernel.
@@ -1497,7 +1508,7 @@ GradLayout grad_layout(const archead_handle& h, int T) {
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
   if (!o.direct) o.rb = take(static_cast<size_t>(o.Kz) * L.d * 2);
-  if (o.own_x) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 2);
+  if (o.own_x) o.rbp = take(static_cast<size_t>(o.Kz) * L.d * 4);
   o.total = at;
   return o;
 }
@@ -1559,10 +1570,10 @@ cudaError_t grad_activations(const GradCall& c, const uint16_t* hidden, GemmPara
   // z = h [R | B]^T: the operand's h carries 2^(c_t - alpha), the rows 2^(sigma - beta|gamma)
   CUtensorMap mx, mr;
   e = tc_encode_map(&mx, xop, L.d, T, Kc, kGM / 2);
-  if (e == cudaSuccess) e = tc_encode_map(&mr, reinterpret_cast<const uint16_t*>(c.wb + c.o.rbp), L.d, c.o.Kz, L.d, kGN / 2);
+  if (e == cudaSuccess) e = tc_encode_map(&mr, reinterpret_cast<const uint16_t*>(c.wb + c.o.rbp), 2 * L.d, c.o.Kz, 2 * L.d, kGN / 2);
   if (e != cudaSuccess) return e;
   p.N = c.o.Kz;
-  p.n_k = L.d / 64;
+  p.n_k = 2 * L.d / 64;
   p.splits = 1;
   p.x = xop + L.d;
   p.mul_acc = std::ldexp(1.f, h.tc_alpha - c.sigma);
