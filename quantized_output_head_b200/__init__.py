@@ -635,8 +635,13 @@ def _check_cu(cu_seqlens, device):
     return cu_seqlens.contiguous(), cu_seqlens.shape[0] - 1
 
 
+_HIDDEN_DTYPES = (torch.bfloat16, torch.int16, torch.uint16)
+
+
 def _check_hidden(hidden: torch.Tensor, d: int) -> None:
-    if hidden.dim() != 2 or hidden.shape[1] != d or hidden.element_size() != 2 or not hidden.is_contiguous():
+    if hidden.dtype not in _HIDDEN_DTYPES:
+        raise ValueError("hidden must be torch.bfloat16 (or its bit patterns as int16 or uint16); convert other types first")
+    if hidden.dim() != 2 or hidden.shape[1] != d or not hidden.is_contiguous():
         raise ValueError(f"hidden must be a contiguous [T, {d}] tensor of 16-bit (bf16) elements")
     if not hidden.is_cuda:
         raise ValueError("hidden must be on the CUDA device")
