@@ -163,10 +163,10 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// exp(x) and exp(x) - 1 - x without its cancellation: argument reduction by
+// exp(x), exp(x) - 1 and exp(x) - 1 - x without their cancellation: argument reduction by
 // multiples of log 2 (Cody and Waite 1980), then the Taylor series, whose
 // remainder after f^10 is below 2^-40 of the value for |f| <= log(2) / 2.
-__device__ __forceinline__ double exp_k3(double x, double& k3) {
+__device__ __forceinline__ double exp_k3(double x, double& m1, double& k3) {
   double r;
   if (fabs(x) < 700.0) {
     const double n = rint(x * 1.4426950408889634);
@@ -183,13 +183,15 @@ __device__ __forceinline__ double exp_k3(double x, double& k3) {
     q = q * f * f;
     if (n == 0.0) {
       k3 = q;
-      return 1.0 + (f + q);
+      m1 = f + q;
+      return 1.0 + m1;
     }
     r = (1.0 + (f + q)) * __hiloint2double((1023 + static_cast<int>(n)) << 20, 0);
   } else {
     r = exp(x);   // overflow, underflow, NaN
   }
-  k3 = r - 1.0 - x;
+  m1 = r - 1.0;   // (not k3 + x: of a large -x nothing of it would be left, of an infinite one NaN)
+  k3 = x > 700.0 ? m1 : m1 - x;   // (x is less than half an ulp there, and infinity less infinity NaN)
   return r;
 }
 
@@ -511,8 +513,8 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
       const double adv = p.per_sequence ? __ldg(p.adv + q[i]) : A[i];
       const double w = by_sequence ? all * a.each[q[i]] : all;
       const double D = static_cast<double>(o[i]) - static_cast<double>(x[i]);
-      double k3;
-      const double ratio = exp_k3(D, k3);
+      double m1, k3;
+      const double ratio = exp_k3(D, m1, k3);
       const bool cut = adv > 0.0 ? D > p.border_hi : adv < 0.0 && D < p.border_lo;
       double l = -adv * (cut ? (adv > 0.0 ? p.clip_hi : p.clip_lo) : ratio), dl = cut ? 0.0 : adv * ratio;
       cut_n += cut ? 1.0 : 0.0;
@@ -520,11 +522,11 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
       if (a.ce_ref != nullptr) {
         const double d = static_cast<double>(x[i]) - static_cast<double>(r[i]);
         double k;
-        exp_k3(d, k);
+        exp_k3(d, m1, k);
         kl_ref += k;
         if (p.kl != 0.0) {   // (0 times an infinite divergence would be NaN)
           l = fma(p.kl, k, l);
-          dl = fma(p.kl, k + d, dl);
+          dl = fma(p.kl, m1, dl);
         }
       }
       loss = fma(w, l, loss);
