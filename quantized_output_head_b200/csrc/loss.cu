@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kLossThreads, 1) policy_loss_kernel(const Poli
       double m1, k3;
       const double ratio = exp_k3(D, m1, k3);
       const bool cut = adv > 0.0 ? D > p.border_hi : adv < 0.0 && D < p.border_lo;
-      double l = -adv * (cut ? (adv > 0.0 ? p.clip_hi : p.clip_lo) : ratio), dl = cut ? 0.0 : adv * ratio;
+      const double gain = adv == 0.0 && ratio == ratio ? 0.0 : adv * ratio;   // (0 times a ratio that overflowed would be NaN)
+      double l = cut ? -adv * (adv > 0.0 ? p.clip_hi : p.clip_lo) : -gain, dl = cut ? 0.0 : gain;
       cut_n += cut ? 1.0 : 0.0;
       kl_old += k3;
       if (a.ce_ref != nullptr) {

@@ -40,3 +40,14 @@ def test_a_token_of_probability_zero(qoh):
     # (and the divergence from the policy that sampled a token it gives probability 0)
     _, g, stats = qoh.policy_loss(dev(1.0, 1.0), dev(INF, 1.0), dev(1.0, 1.0), reduction="sum")
     assert g[0] == 0 and g[1] == 1.0 and stats[0] == 0.5 and stats[1] == INF
+
+
+@pytest.mark.parametrize("reduction", ["tokens", "sequences", "sum"])
+def test_no_advantage_no_loss(qoh, reduction):
+    """An advantage of 0 (a group whose rewards are all equal) has no part in the loss, however large the ratio."""
+    ce, old = dev(0.0, 0.0, 5.0, 1.0), dev(800.0, 3.4e38, 2.0, 1.0)
+    loss, g, _ = qoh.policy_loss(ce, old, torch.zeros_like(ce), reduction=reduction)
+    assert loss == 0 and not g.any()
+    # (a NaN that counts is not hidden)
+    loss, g, _ = qoh.policy_loss(dev(float("nan"), 1.0), dev(1.0, 1.0), dev(0.0, 0.0), reduction=reduction)
+    assert torch.isnan(loss) and torch.isnan(g[0])
