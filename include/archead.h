@@ -309,7 +309,12 @@ ARCHEAD_API int archead_merge_sample_shards(const float* sample_partials, int32_
  * result is this shard's share, to be added over the shards (in fp32).
  * workspace: >= archead_grad_workspace_bytes(handle, T), 256-byte aligned; the
  * call needs nothing in it and leaves its own status bits in the status word
- * (archead_workspace_status).  Calls that may overlap need one each. */
+ * (archead_workspace_status).  Calls that may overlap need one each.  The size is
+ * that of the kernels a call of T tokens takes and does not grow with T
+ * throughout (8 tokens of a 262144 x 2560 head need 27 MB, 9 need 21): one
+ * workspace for calls of several T has to be as large as the largest of their
+ * sizes, a smaller one is refused (ENOMEM).  0 if handle is NULL or T is not in
+ * [1, 2^20]. */
 enum { ARCHEAD_GRAD_BF16 = 0, ARCHEAD_GRAD_F32 = 1 };
 ARCHEAD_API size_t archead_grad_workspace_bytes(const archead_handle* handle, int32_t T);
 ARCHEAD_API int archead_grad_hidden(const archead_handle* handle, const uint16_t* hidden, int32_t T,

@@ -336,6 +336,8 @@ class PackedHead:
 
     # ------------------------------------------------------------ gradient
     def grad_workspace_bytes(self, T: int) -> int:
+        """Workspace of a grad_hidden call of T tokens.  Not monotone in T: one workspace for
+        several T takes the largest of their sizes."""
         return int(_lib.archead_grad_workspace_bytes(self.handle, int(T)))
 
     def grad_hidden(self, hidden: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor, grad_ce: torch.Tensor,
