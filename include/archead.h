@@ -299,7 +299,10 @@ ARCHEAD_API int archead_merge_sample_shards(const float* sample_partials, int32_
  *   grad_ce     [T] fp32, g.  A token with g = 0 gets a row of zeros whatever
  *               its target, lse and hidden state hold (masked tokens).
  *   grad_hidden [T, d], 16-byte aligned, bf16 bit patterns or fp32 by
- *               grad_dtype; every row is written.
+ *               grad_dtype; every row is written.  The products' operands are
+ *               fp16 and their sums fp32, so a row is good to about 2^-11 of its
+ *               norm in either type: fp32 is for adding up shards and leaves out
+ *               bf16's own rounding (2^-8), it is not a gradient of fp32 accuracy.
  * A target outside [0, V) with g != 0 gives a row of NaN and sets
  * ARCHEAD_STATUS_BAD_TARGET.  The probabilities are normalised by their own sum,
  * so lse may be that of any of the forward calls; one that is off by log 2 or

@@ -347,7 +347,8 @@ class PackedHead:
         lse_argmax(hidden, targets) gave with lse [T] (fp32).  The head is
         frozen.  A token with grad_ce 0 gets zeros whatever its target and lse
         hold.  out_dtype: bfloat16, or float32 (to add up vocabulary shards,
-        whose lse is the merged one).  workspace: a uint8 tensor of
+        whose lse is the merged one); a row is good to about 2^-11 of its norm
+        before that rounding, the operands of the products being fp16.  workspace: a uint8 tensor of
         grad_workspace_bytes(T) on this device, for callers that want its status
         word (status()); by default one is allocated for the call."""
         _check_hidden(hidden, self.d)

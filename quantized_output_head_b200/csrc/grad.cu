@@ -28,7 +28,7 @@
 //   2. gemm softmax          G of the chunk, fp16
 //   3. gemm accumulate       dX += G W~, fp32
 // and after the last chunk
-//   4. dx_kernel             dX / S + (1/S - 1) W~[target], its low-rank
+//   4. dx_kernel             dX / S - (Rest / S) W~[target], its low-rank
 //      columns to fp16; lowrank_rows_kernel: [s_R R | s_B B], fp16
 //   5. gemm finish           dh from dX_res + dz [s_R R | s_B B].
 // Few tokens: G from the forward kernels, gw_kernel for G W~, then 4 and 5; up to
@@ -36,9 +36,13 @@
 //
 // Roundings to fp16: W~ entries (2^-11 relative, as in the forward), G (2^-11,
 // stored times 2^15 so that a probability keeps its full precision down to
-// 2^-29), dX of the low-rank columns and the rows of R and B.  All are
-// independent from entry to entry, so the sum's error stays near 2^-12 of its
-// own size, below the bf16 rounding of the result; sums are fp32.
+// 2^-29), dX of the low-rank columns and the rows of R and B (for dh; z takes them
+// exactly).  fp16 because the tensor cores take no operand of more than 11 bits
+// (tf32 has the same 11, at half the rate; bf16 has 8), and a second fp16 term
+// for the rest of each operand would double the products for bits that the bf16
+// result drops.  All are independent from entry to entry, so the sum's error
+// stays near 2^-12 of its own size, below the bf16 rounding of the result; sums
+// are fp32.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -56,9 +60,10 @@ namespace {
 
 constexpr int kGradTokens = 4096;     // tokens of one pass over the head
 // Vocabulary rows of one pass: as many as keep the W~ chunk and the G chunk near
-// these sizes (35,840 rows at 4096 tokens and 4672 columns).  Fewer passes re-read
-// and re-write dX less often and leave fewer part-filled rounds of tiles: 29, 17,
-// 9 and 5 passes took 9.1, 8.5, 8.2 and 7.9 ms for the chunks' kernels.
+// these sizes, evened out over the passes (4096 tokens of 151936 x 4096, 4672
+// columns: 35,840 rows fit, five passes of 30,464).  Fewer passes re-read and
+// re-write dX less often and leave fewer part-filled rounds of tiles: 29, 17, 9 and
+// 5 passes took 9.1, 8.5, 8.2 and 7.9 ms for the chunks' kernels there.
 constexpr size_t kGradWBytes = size_t(320) << 20, kGradGBytes = size_t(512) << 20;
 constexpr int kGradScale = kTcGradScale;   // G is stored times 2^15
 

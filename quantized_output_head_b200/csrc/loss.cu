@@ -163,9 +163,11 @@ __device__ __forceinline__ double warp_sum(double v) {
 }
 __device__ __forceinline__ int warp_sum(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// exp(x), exp(x) - 1 and exp(x) - 1 - x without their cancellation: argument reduction by
-// multiples of log 2 (Cody and Waite 1980), then the Taylor series, whose
-// remainder after f^10 is below 2^-40 of the value for |f| <= log(2) / 2.
+// exp(x), exp(x) - 1 and exp(x) - 1 - x without their cancellation: the argument less
+// a multiple n of log 2 (one fused step; the constant is off by up to 2^-54, which
+// moves the value by n 2^-54, 2^-44 at |x| = 700), then the Taylor series up to f^10.
+// What that leaves out is below 2^-41 of exp(x), 2^-40 of exp(x) - 1 and 2^-37 of
+// exp(x) - 1 - x, for |f| <= log(2) / 2.
 __device__ __forceinline__ double exp_k3(double x, double& m1, double& k3) {
   double r;
   if (fabs(x) < 700.0) {
