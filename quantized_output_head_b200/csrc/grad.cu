@@ -1761,10 +1761,15 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
 
 constexpr int kMaxTokens = 1 << 20;
 
-}  // namespace
-
-cudaError_t grad_set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(grad_gemm_kernel<kSoftmax>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
+// Shared-memory limits of the kernels, at a head's first gradient call: at its
+// construction they would load a dozen kernels for programs that only infer (whose
+// first head took 15 ms in place of 9).  Calls that race
+// set them twice.
+cudaError_t grad_set_attributes(const archead_handle& h) {
+  if (__atomic_load_n(&h.grad_ready, __ATOMIC_ACQUIRE) != 0) return cudaSuccess;
+  cudaError_t e = h.tc_ok ? tc_set_grad_attributes() : cudaSuccess;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(grad_gemm_kernel<kSoftmax>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(grad_gemm_kernel<kLowrank>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGSmem);
   if (e == cudaSuccess)
@@ -1774,8 +1779,11 @@ cudaError_t grad_set_attributes() {
   for (const void* k : {reinterpret_cast<const void*>(&gw_kernel<1>), reinterpret_cast<const void*>(&gw_kernel<2>),
                         reinterpret_cast<const void*>(&gw_kernel<4>), reinterpret_cast<const void*>(&gw_kernel<8>)})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGwSmem);
+  if (e == cudaSuccess) __atomic_store_n(&h.grad_ready, 1, __ATOMIC_RELEASE);
   return e;
 }
+
+}  // namespace
 
 }  // namespace archead
 
@@ -1805,6 +1813,8 @@ extern "C" ARCHEAD_API int archead_grad_hidden(const archead_handle* handle, con
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return set_cuda_error(e);
   if (dev != handle->device) return ARCHEAD_EINVAL;
+  e = grad_set_attributes(*handle);
+  if (e != cudaSuccess) return set_cuda_error(e);
   return grad_launch(*handle, o, hidden, T, targets, lse, grad_ce, grad_hidden, grad_dtype == ARCHEAD_GRAD_F32,
                      static_cast<uint8_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
 }

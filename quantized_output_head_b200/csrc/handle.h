@@ -34,6 +34,7 @@ struct archead_handle {
   uint64_t wait_limit_ns;   // decode kernel: limit of every bounded wait (test hook; default kWaitLimitNs)
   int test_stall;           // decode kernel: test hook, a wait that nothing completes
   struct HostGraphCache* graphs;   // host-buffer entry points: captured sequences (api.cu), owned
+  mutable int grad_ready;   // the gradient's kernels are set up (at its first call)
 };
 
 namespace archead {
@@ -137,7 +138,8 @@ int act_prep_splits(int T, int d, int Kc, int num_sms, size_t scratch_bytes);
 void tc_smem_plan(TcParams& p);
 size_t tc_smem_bytes(const TcParams& p);
 size_t tc_smem_max();
-cudaError_t tc_set_attributes();
+cudaError_t tc_set_attributes();        // of the forward's instances
+cudaError_t tc_set_grad_attributes();   // of the gradient's
 cudaError_t tc_encode_map(CUtensorMap* map, const uint16_t* base, uint64_t cols, uint64_t rows, uint64_t pitch,
                           int box_rows);
 cudaError_t tc_encode_xmap(CUtensorMap* map, const uint16_t* xop, int T, int Kc, int BN);
@@ -156,9 +158,6 @@ int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float
 // probabilities in place of logits.
 int forward_tc_grad(const archead_handle& h, const uint16_t* hidden, int T, const int32_t* targets, const float* lse,
                     const float* grad, void* G, float* ssum, float* ptgt, void* ws, cudaStream_t stream);
-
-// Gradient of the head (grad.cu).
-cudaError_t grad_set_attributes();
 
 // Thread-local record of the last CUDA error (api.cu).
 int set_cuda_error(cudaError_t e);

@@ -328,7 +328,6 @@ extern "C" ARCHEAD_API int archead_pack_load(const archead_desc* desc, const arc
   plan_tc(h, *comps, optin);
   e = decode_set_attributes(L.g_steps, static_cast<size_t>(optin));
   if (e == cudaSuccess && h->tc_ok) e = tc_set_attributes();
-  if (e == cudaSuccess) e = grad_set_attributes();
   if (e != cudaSuccess) {
     delete h;
     return set_cuda_error(e);

@@ -797,6 +797,12 @@ cudaError_t tc_set_attributes() {
   cudaError_t e = cudaSuccess;
   for (int r = kTcMinRing; r <= kTcMaxRing && e == cudaSuccess; ++r)
     e = cudaFuncSetAttribute(tc_kernel_for<false>(r), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e;
+}
+
+cudaError_t tc_set_grad_attributes() {
+  const int smem = static_cast<int>(tc_smem_max());
+  cudaError_t e = cudaSuccess;
   for (int r = kTcMinRing; r <= kTcMaxRing && e == cudaSuccess; ++r)
     e = cudaFuncSetAttribute(tc_kernel_for<true>(r), cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
