@@ -852,55 +852,54 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
 }
 
 // ------------------------------------------------------- few tokens: G, G W~
-// G from the forward kernels' logits (fp32 [T][V]), in the order gw_kernel loads
-// it: pieces of 32 tokens x 128 rows of the head (8 KB), in a piece 16-byte runs
-// of 8 rows, the 32 tokens of a run side by side, so that a warp's load of one
-// run per lane (= token) is 512 contiguous bytes.  (Read row by row, 16 bytes of
-// 32 rows per load, G cost gw_kernel 37 of 161 us at 64 tokens.)  One block per
-// piece, with its tokens' sums of G and, where the target is one of the rows, its
-// exp(y - lse).
+// The order in which gw_kernel loads G: pieces of 32 tokens x 128 rows of the head
+// (8 KB), in a piece 16-byte runs of 8 rows, the 32 tokens of a run side by side, so
+// that a warp's load of one run per lane (= token) is 512 contiguous bytes.  (Read
+// row by row, 16 bytes of 32 rows per load, G cost gw_kernel 37 of 161 us at 64
+// tokens.)  The tensor-core forward writes it from its epilogue; for the few tokens
+// of the decode kernel g_kernel makes it from the logits (fp32 [T][V]): one block
+// per piece, one warp per token, with the token's sum of G and, where the target is
+// one of the rows, its exp(y - lse); the piece's other tokens are zeros.
 struct GParams {
   const float* y;
   const float* lse;
   const float* grad;
   const int32_t* targets;
-  uint4* G;                   // [k-step][T / 32][16][32]
+  uint4* G;                   // [k-step][16][32]
   float* ssum;                // [T][ssum_pitch], one per k-step
   float* ptgt;                // [T]
-  int32_t T, V, row0, ssum_pitch;
+  int32_t T, V, row0, ssum_pitch;   // T <= kDecodeTokens
 };
 constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
-__global__ void __launch_bounds__(256) g_kernel(const GParams p) {
-  __shared__ __align__(16) uint16_t piece[kGwRows / 8][32][8];
+static_assert(kTcMinTokens <= kDecodeTokens + 1, "a token per warp of g_kernel");
+__global__ void __launch_bounds__(32 * kDecodeTokens) g_kernel(const GParams p) {
+  __shared__ __align__(16) uint16_t piece[kGwRows / 8][kDecodeTokens][8];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = blockIdx.x * kGwRows;
+  const int t = threadIdx.x >> 5, lane = threadIdx.x & 31, v0 = blockIdx.x * kGwRows;
+  const bool live = t < p.T && p.grad[t] != 0.f;   // (its lse and target may be anything otherwise)
+  const float lse = live ? p.lse[t] : 0.f;
+  const int target = live ? p.targets[t] - p.row0 : -1;
+  const float* y = p.y + static_cast<size_t>(t) * p.V;
+  float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tl = 4 * warp + i, t = 32 * blockIdx.y + tl;
-    const bool live = t < p.T && p.grad[t] != 0.f;   // (its lse and target may be anything otherwise)
-    const float lse = live ? p.lse[t] : 0.f;
-    const int target = live ? p.targets[t] - p.row0 : -1;
-    const float* y = p.y + static_cast<size_t>(t) * p.V;
-    float sum = 0.f;
-#pragma unroll
-    for (int e = 0; e < kGwRows / 32; ++e) {
-      const int v = v0 + 32 * e + lane;
-      float x = live && v < p.V ? __expf(y[v] - lse) : 0.f;
-      if (live && v == target) {
-        if (v < p.V) p.ptgt[t] = x;
-        x = 0.f;
-      }
-      sum += x;
-      piece[4 * e + (lane >> 3)][tl][lane & 7] = __half_as_ushort(__float2half_rn(x * static_cast<float>(1 << kGradScale)));
+  for (int e = 0; e < kGwRows / 32; ++e) {
+    const int v = v0 + 32 * e + lane;
+    float x = live && v < p.V ? __expf(y[v] - lse) : 0.f;
+    if (live && v == target) {
+      if (v < p.V) p.ptgt[t] = x;
+      x = 0.f;
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0 && t < p.T) p.ssum[static_cast<size_t>(t) * p.ssum_pitch + blockIdx.x] = sum;
+    sum += x;
+    piece[4 * e + (lane >> 3)][t][lane & 7] = __half_as_ushort(__float2half_rn(x * static_cast<float>(1 << kGradScale)));
   }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0 && t < p.T) p.ssum[static_cast<size_t>(t) * p.ssum_pitch + blockIdx.x] = sum;
   __syncthreads();
-  uint4* dst = p.G + (static_cast<size_t>(blockIdx.x) * gridDim.y + blockIdx.y) * (kGwRows / 8 * 32);
-  for (int i = threadIdx.x; i < kGwRows / 8 * 32; i += blockDim.x) dst[i] = reinterpret_cast<const uint4*>(piece)[i];
+  uint4* dst = p.G + static_cast<size_t>(blockIdx.x) * (kGwRows / 8 * 32);
+  for (int i = threadIdx.x; i < kGwRows / 8 * 32; i += blockDim.x)
+    dst[i] = lane < kDecodeTokens ? *reinterpret_cast<const uint4*>(piece[i >> 5][lane]) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // dX = G W~ for up to 128 tokens, the packed rows dequantised on the way:
@@ -932,7 +931,7 @@ constexpr uint32_t kGwSmem = kGwBarOff + 512 + 1024;
 
 struct GwParams {
   DequantParams rows;
-  const uint4* G;              // in g_kernel's order, zeros past the last row of the head
+  const uint4* G;              // in that order, zeros past the last row of the head
   int32_t T;
   int32_t n_mtiles, nk;        // k-steps of kGwRows rows
   int32_t chunks;              // 64-column chunks in all
@@ -1662,7 +1661,7 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
     const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
     if (rc != ARCHEAD_OK) return rc;
     GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, p.ptgt, T, L.V, h.row0, p.ssum_pitch};
-    e = launch_after(g_kernel, dim3(c.o.n_ssum, (T + 31) / 32), 256, 0, c.stream, gp);
+    e = launch_after(g_kernel, dim3(c.o.n_ssum), 32 * kDecodeTokens, 0, c.stream, gp);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
   const GwPlan g = gw_plan(h);
@@ -1763,8 +1762,7 @@ constexpr int kMaxTokens = 1 << 20;
 
 // Shared-memory limits of the kernels, at a head's first gradient call: at its
 // construction they would load a dozen kernels for programs that only infer (whose
-// first head took 15 ms in place of 9).  Calls that race
-// set them twice.
+// first head took 15 ms in place of 9).  Calls that race set them twice.
 cudaError_t grad_set_attributes(const archead_handle& h) {
   if (__atomic_load_n(&h.grad_ready, __ATOMIC_ACQUIRE) != 0) return cudaSuccess;
   cudaError_t e = h.tc_ok ? tc_set_grad_attributes() : cudaSuccess;
