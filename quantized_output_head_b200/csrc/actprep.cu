@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(256, 1) act_prep_kernel(const ActParams p) {
     if (lane == 0) {
       int E = 0;
       if (m16 != 0) frexpf(__uint_as_float(m16 << 16), &E);   // max|h_t| < 2^E
-      s_E[tl] = E;
+      s_E[tl] = max(E, kMinExp);
       s_nz[tl] = m16 != 0;
     }
   }

@@ -345,7 +345,7 @@ __device__ void residual_warp(const DecodeParams& p, const SmemView& sv, int n_m
   if (tok) {
     int E = 0;
     frexpf(mx, &E);
-    hs = ldexpf(1.f, kScaleExp - E);
+    hs = ldexpf(1.f, kScaleExp - max(E, kMinExp));
   }
   // fp16 h fragments of this warp's columns, and the constant-part sum of each
   // local group for token gr.

@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(128) x_hidden_kernel(const XParams p) {
   m = max(max(part[0], part[1]), max(part[2], part[3]));
   int E = 0;
   if (m != 0) frexpf(__uint_as_float(m << 16), &E);   // max|h_t| < 2^E
+  E = max(E, kMinExp);
   if (threadIdx.x == 0) p.cinv[t] = ldexpf(1.f, E - kScaleExp - p.mseg);
   const float s = ldexpf(1.f, kScaleExp - E + p.mseg - p.alpha);
   for (int e = threadIdx.x; e < p.d; e += 128) {

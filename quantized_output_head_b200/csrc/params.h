@@ -23,6 +23,9 @@ constexpr int kRing = 4;                 // m-tiles in flight per compute warp
 // prologue's E_t, a residual warp's own columns in the decode kernel), so
 // they stay below 2^kScaleExp.
 constexpr int kScaleExp = 14;
+// E is at least this: 2^(kScaleExp - E) has to be a float (from E = -114 down it would
+// be infinite, and its product with a zero of h NaN).
+constexpr int kMinExp = -96;
 
 struct DecodeParams {
   const uint8_t* mtiles;       // arena: m-tile blocks
