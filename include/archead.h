@@ -309,7 +309,10 @@ ARCHEAD_API int archead_merge_sample_shards(const float* sample_partials, int32_
  * more may give NaN.  On a vocabulary shard (archead_set_vocab_shard with more
  * rows than this head's) that sum is not known: lse is the log-sum-exp over all
  * rows (archead_merge_shards), taken as it is, targets are global, and the
- * result is this shard's share, to be added over the shards (in fp32).
+ * result is this shard's share, to be added over the shards (in fp32).  What lse is
+ * off by reaches it: 1 - p of a sure target is good to about 2^-22 |lse| with the
+ * lse of archead_shard_partials on the same kernels, the logits being recomputed
+ * on those (heads with g_B no multiple of 64: 8 tokens a pass over the head).
  * workspace: >= archead_grad_workspace_bytes(handle, T), 256-byte aligned; the
  * call needs nothing in it and leaves its own status bits in the status word
  * (archead_workspace_status).  Calls that may overlap need one each.  The size is

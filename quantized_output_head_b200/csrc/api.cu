@@ -41,7 +41,7 @@ struct TcGradArgs {
   const int32_t* targets;
   void* G;
   float* ssum;
-  float* ptgt;
+  float* ltgt;
 };
 
 // Tensor-core path: activation operand, the tensor-core kernel, and the
@@ -117,7 +117,7 @@ int forward_tc(const archead_handle* h, const uint16_t* hidden, int32_t T, const
     tp.grad = grad->grad;
     tp.G = static_cast<uint4*>(grad->G);
     tp.ssum = grad->ssum;
-    tp.ptgt = grad->ptgt;
+    tp.ltgt = grad->ltgt;
   }
   tc_smem_plan(tp);
   CUtensorMap map;
@@ -282,10 +282,10 @@ int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float
 }
 
 int forward_tc_grad(const archead_handle& h, const uint16_t* hidden, int T, const int32_t* targets, const float* lse,
-                    const float* grad, void* G, float* ssum, float* ptgt, void* ws, cudaStream_t stream) {
+                    const float* grad, void* G, float* ssum, float* ltgt, void* ws, cudaStream_t stream) {
   archead_handle q = h;
   q.ev_before = q.ev_after = nullptr;
-  const TcGradArgs ga{lse, grad, targets, G, ssum, ptgt};
+  const TcGradArgs ga{lse, grad, targets, G, ssum, ltgt};
   return forward_tc(&q, hidden, T, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, static_cast<uint8_t*>(ws),
                     ws_layout(q, T), stream, &ga);
 }

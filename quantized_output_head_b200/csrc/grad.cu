@@ -20,8 +20,12 @@
 // No term cancels: with the target's p - 1 inside G, its coefficient 1 - p of a
 // confident token would be a difference of terms of size |S - 1| that are rounded
 // to fp16 (rows of 1 - p = 1e-5 were 45 % off with lse off by 1e-2).
-// (On a vocabulary shard S is not known: lse is taken as it is, the coefficient
-// is p - 1.)
+// On a vocabulary shard S is not known: lse is taken as it is, and the coefficient
+// is p - 1, from y - lse in one rounding.  Of a sure token it is as good as y and
+// lse agree, so a shard's logits come from the kernels that gave its lse: the
+// activation kernel's z at every token count, and on heads that the tensor-core
+// forward does not take the decode kernel's logits, 8 tokens a pass (rows of
+// 1 - p = 1e-2 were up to 39 % off with the fp16 rows' logits there, 0.06 % now).
 //
 // Many tokens: the vocabulary is walked in chunks of rows.  Per chunk
 //   1. dequant_rows_kernel   W~ of the chunk, fp16, in the workspace
@@ -169,9 +173,8 @@ struct LowrankParams {
   float mul_c, mul_r;
 };
 // (For z a row is the sum of two fp16 ones: a code times an fp16 scale has at most 19
-// bits, so the pair is exact and z is that of the forward's activation kernel.  The
-// rounded rows alone move the logits by up to 2^-11 of their size, which a vocabulary
-// shard, whose probabilities nothing normalises, would carry into its gradient.)
+// bits, so the pair is exact and z is as good as the forward's activation kernel's.
+// The rounded rows alone move the logits by up to 2^-11 of their size.)
 // A thread per 8 columns; the first block also clears the workspace header.
 __global__ void __launch_bounds__(256) lowrank_rows_kernel(const LowrankParams p) {
   if (blockIdx.x == 0 && threadIdx.x < 64) p.header[threadIdx.x] = 0u;
@@ -299,7 +302,7 @@ __host__ __device__ __forceinline__ int gw_splits(const GwSplits& g, int block) 
 struct DxParams {
   DequantParams rows;
   const float* ssum;          // [tokens][ssum_pitch], n_ssum of them used
-  const float* ptgt;          // [tokens]
+  const float* ltgt;          // [tokens]: log of the target's probability
   const float* grad;
   const int32_t* targets;
   float* dx;
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
       v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
     }
   }
-  const float own = here ? p.ptgt[t] : 0.f;
-  float r = 1.f, c = own - 1.f;
+  const float own = here ? p.ltgt[t] : 0.f;
+  float r = 1.f, c = here ? expm1f(own) : 0.f;
   if (p.whole) {
     const float* parts = p.ssum + static_cast<size_t>(t) * p.ssum_pitch;
     float s = 0.f;
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(256) dx_kernel(const DxParams p) {
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += part[i];
-    r = 1.f / (s + own);
+    r = 1.f / (s + expf(own));
     c = -s * r;
   }
   if (!out) return;
@@ -442,7 +445,7 @@ struct GemmParams {
   int32_t pitch, v0, V;                // first row of the chunk, rows of the head
   float* ssum;                         // [tokens][ssum_pitch]: sums of G over half a tile's rows
   int32_t ssum_pitch;
-  float* ptgt;                         // [tokens]: exp(y - lse) of the target's row
+  float* ltgt;                         // [tokens]: y - lse of the target's row
   uint16_t* x;                         // lowrank: z columns of X, [M][Kc]
   // accumulate / finish
   float* dx;                           // [splits][M][Kc]
@@ -663,6 +666,14 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
           // columns are vocabulary rows of the chunk; a token without a
           // gradient gets zeros (its lse and target may be anything)
           const int tl = target - p.row0 - p.v0 - n0 - c0, left = p.V - p.v0 - n0 - c0;
+          const bool own = g != 0.f && tl >= 0 && tl < 32, any = __any_sync(0xffffffffu, own) != 0;
+          if (any) {   // in one rounding: on a shard exp(y - lse) - 1 is taken of it
+            float acc_t = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c == tl) acc_t = __uint_as_float(r[c]);
+            if (own) p.ltgt[t] = fmaf(acc_t, cinv, -lse);
+          }
           float x[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = exp2_approx(fmaf(__uint_as_float(r[c]), k2, -l2));
@@ -674,16 +685,10 @@ __device__ void g_epilogue(const GemmParams& p, const GemmSmem& sm, uint32_t tme
             for (int c = 0; c < 32; ++c)
               if (c >= left) x[c] = 0.f;
           }
-          const bool own = g != 0.f && tl >= 0 && tl < 32;
-          if (__any_sync(0xffffffffu, own)) {
-            float pt = 0.f;
+          if (any) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c == tl) {
-                pt = x[c];
-                x[c] = 0.f;
-              }
-            if (own) p.ptgt[t] = pt * (1.f / (1 << kGradScale));
+              if (c == tl) x[c] = 0.f;
           }
 #pragma unroll
           for (int c = 0; c < 32; c += 4) ssum += (x[c] + x[c + 1]) + (x[c + 2] + x[c + 3]);
@@ -860,7 +865,7 @@ cudaError_t launch_gemm(GemmParams& p, const CUtensorMap& ma, const CUtensorMap&
 // tokens.)  The tensor-core forward writes it from its epilogue; for the few tokens
 // of the decode kernel g_kernel makes it from the logits (fp32 [T][V]): one block
 // per piece, one warp per token, with the token's sum of G and, where the target is
-// one of the rows, its exp(y - lse); the piece's other tokens are zeros.
+// one of the rows, its y - lse; the piece's other tokens are zeros.
 struct GParams {
   const float* y;
   const float* lse;
@@ -868,7 +873,7 @@ struct GParams {
   const int32_t* targets;
   uint4* G;                   // [k-step][16][32]
   float* ssum;                // [T][ssum_pitch], one per k-step
-  float* ptgt;                // [T]
+  float* ltgt;                // [T]
   int32_t T, V, row0, ssum_pitch;   // T <= kDecodeTokens
 };
 constexpr int kGwRows = 128, kGwMt = kGwRows / kMT;   // rows and m-tiles of a k-step
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(32 * kDecodeTokens) g_kernel(const GParams p) 
     const int v = v0 + 32 * e + lane;
     float x = live && v < p.V ? __expf(y[v] - lse) : 0.f;
     if (live && v == target) {
-      if (v < p.V) p.ptgt[t] = x;
+      if (v < p.V) p.ltgt[t] = y[v] - lse;
       x = 0.f;
     }
     sum += x;
@@ -1408,7 +1413,7 @@ __global__ void __launch_bounds__(512) finish_few_kernel(const FinishFewParams p
 // in one chunk, 65531 x 1024: 160 to 198 us against 142).
 constexpr int kFewPass = 128;
 
-// Many tokens of a head with low-rank rows: z by a product with the rows of R and B
+// Many tokens of a whole head with low-rank rows: z by a product with the rows of R and B
 // (pairs of fp16 rows) from this many tokens on, below by the activation kernel,
 // which has one launch less (whole gradient, 151936 x 4096: 1024 tokens 2.94
 // against 2.97 ms, 4096 tokens 9.65 against 9.83 ms; 32003 x 2048: 1024 tokens 374
@@ -1467,7 +1472,7 @@ struct GradLayout {
   bool own_x;                      // X by x_hidden_kernel and a product
   int tokens, chunk, splits, Kz;   // tokens and vocabulary rows per pass; partial dX (K splits)
   int pitch, n_ssum;
-  size_t fwd, logits, cinv, ssum, ptgt, xop, w, g, dx, dz, rb, rbp, total;
+  size_t fwd, logits, cinv, ssum, ltgt, xop, w, g, dx, dz, rb, rbp, total;
 };
 
 GradLayout grad_layout(const archead_handle& h, int T) {
@@ -1481,10 +1486,11 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     at += round_up(bytes, 256);
     return r;
   };
+  const bool whole = h.v_total == L.V;
   const size_t rows = std::max<size_t>(4096, std::min(kGradWBytes / (2 * Kc), kGradGBytes / (2 * std::min(T, kGradTokens))));
   // (without the tensor-core forward a pass of its logits takes 8 tokens)
-  o.few = h.tc_ok ? T <= kFewPass || (T <= 2 * kFewPass && static_cast<size_t>(L.Vp) > rows) : T <= kDecodeTokens;
-  const int passes = (T + kFewPass - 1) / kFewPass;
+  o.few = h.tc_ok ? T <= kFewPass || (T <= 2 * kFewPass && static_cast<size_t>(L.Vp) > rows) : T <= kDecodeTokens || !whole;
+  const int pass = h.tc_ok ? kFewPass : kDecodeTokens, passes = (T + pass - 1) / pass;
   const size_t t = o.few ? (T + passes - 1) / passes : std::min(T, kGradTokens);
   o.tokens = static_cast<int>(t);
   o.direct = t <= kDecodeTokens;
@@ -1502,13 +1508,13 @@ GradLayout grad_layout(const archead_handle& h, int T) {
     o.pitch = o.chunk + 64;   // (a power of two between G's rows would send a whole box to one memory channel)
     o.n_ssum = 2 * ((L.Vp + kGN - 1) / kGN);
     o.splits = accumulate_splits(o.tokens, Kc, o.chunk, h.num_sms / 2);
-    o.own_x = !h.tc_ok || (o.Kz > 0 && t >= kOwnXTokens);
+    o.own_x = !h.tc_ok || (whole && o.Kz > 0 && t >= kOwnXTokens);
     o.cinv = take(t * 4);
     o.xop = take(t * Kc * 2);
     o.w = take(static_cast<size_t>(o.chunk) * Kc * 2);
   }
   o.ssum = take(t * (o.few ? 4 * o.n_ssum : round_up(o.n_ssum, 4)) * 4);
-  o.ptgt = take(t * 4);
+  o.ltgt = take(t * 4);
   o.g = take(o.few ? static_cast<size_t>(o.n_ssum) * kGwRows * round_up(t, 32) * 2 : t * o.pitch * 2);
   o.dx = take(static_cast<size_t>(o.splits) * t * Kc * 4);
   o.dz = take(t * o.Kz * 2);
@@ -1611,7 +1617,7 @@ int grad_finish(const GradCall& c, GemmParams& p, int n_ssum, int splits, const 
   const Layout& L = c.h.L;
   const int Kc = tc_kc(L), Kz = c.o.Kz, nt = p.M;
   uint16_t* dz = reinterpret_cast<uint16_t*>(c.wb + c.o.dz);
-  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.ptgt, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
+  DxParams dp{dequant_params(c.h, nullptr), p.ssum, p.ltgt, p.grad, p.targets, p.dx, p.split_stride, dz, n_ssum, p.ssum_pitch, Kc, L.d,
               L.V, c.h.row0, c.h.v_total == L.V ? 1 : 0, splits, gw};
   const bool ways = nt <= kDxWaysTokens;
   const auto dx = ways ? dx_kernel<kDxWays> : dx_kernel<1>;
@@ -1655,13 +1661,13 @@ int grad_few(const GradCall& c, const uint16_t* hidden, GemmParams& p) {
   if (use_tc(h, T)) {
     n_ssum *= 4;
     p.ssum_pitch = n_ssum;
-    const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, p.ptgt, c.wb, c.stream);
+    const int rc = forward_tc_grad(h, hidden, T, p.targets, p.lse, p.grad, p.G, p.ssum, p.ltgt, c.wb, c.stream);
     if (rc != ARCHEAD_OK) return rc;
   } else {
     float* logits = reinterpret_cast<float*>(c.wb + c.o.logits);
     const int rc = forward_logits(h, hidden, T, logits, c.wb, c.o.fwd, c.stream);
     if (rc != ARCHEAD_OK) return rc;
-    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, p.ptgt, T, L.V, h.row0, p.ssum_pitch};
+    GParams gp{logits, p.lse, p.grad, p.targets, reinterpret_cast<uint4*>(p.G), p.ssum, p.ltgt, T, L.V, h.row0, p.ssum_pitch};
     e = launch_after(g_kernel, dim3(c.o.n_ssum), 32 * kDecodeTokens, 0, c.stream, gp);
     if (e != cudaSuccess) return set_cuda_error(e);
   }
@@ -1748,7 +1754,7 @@ int grad_launch(const archead_handle& h, const GradLayout& o, const uint16_t* hi
     p.V = L.V;
     p.ssum = reinterpret_cast<float*>(wb + o.ssum);
     p.ssum_pitch = static_cast<int32_t>(round_up(o.n_ssum, 4));   // 16-byte rows
-    p.ptgt = reinterpret_cast<float*>(wb + o.ptgt);
+    p.ltgt = reinterpret_cast<float*>(wb + o.ltgt);
     p.dx = reinterpret_cast<float*>(wb + o.dx);
     p.Kc = tc_kc(L);
     p.split_stride = static_cast<size_t>(nt) * p.Kc;

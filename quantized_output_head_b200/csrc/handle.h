@@ -155,9 +155,9 @@ int forward_logits(const archead_handle& h, const uint16_t* hidden, int T, float
                    cudaStream_t stream);
 
 // The tensor-core kernel's gradient instance (T <= kTcMaxBN, tc_ok): G, its sums and the targets' own
-// probabilities in place of logits.
+// log-probabilities in place of logits.
 int forward_tc_grad(const archead_handle& h, const uint16_t* hidden, int T, const int32_t* targets, const float* lse,
-                    const float* grad, void* G, float* ssum, float* ptgt, void* ws, cudaStream_t stream);
+                    const float* grad, void* G, float* ssum, float* ltgt, void* ws, cudaStream_t stream);
 
 // Thread-local record of the last CUDA error (api.cu).
 int set_cuda_error(cudaError_t e);

@@ -54,7 +54,7 @@ struct TcParams {
   const float* grad;          // [T]
   uint4* G;                   // [128-row tile][ceil(T / 32)][16 runs of 8 rows][32 tokens]
   float* ssum;                // [T][128-row tile][4]: sums of exp(y - lse) over 32 rows, the target's left out
-  float* ptgt;                // [T]: exp(y - lse) of the target's row, where it is one of these
+  float* ltgt;                // [T]: y - lse of the target's row, where it is one of these
 };
 
 struct ActParams {

@@ -534,7 +534,7 @@ __device__ void mma_warp(const TcParams& p, const TcSmem& sm, uint32_t tmem_base
 // kGrad: what goes out is the gradient's G = exp(y - lse), 0 at the target's row,
 // fp16 times 2^kTcGradScale, a lane's token and 8 rows in one 16-byte run (the
 // runs of 32 tokens side by side), its sum over the 32 rows, and the target's own
-// exp(y - lse) by itself.
+// y - lse by itself (in one rounding: on a shard exp(y - lse) - 1 is taken of it).
 template <bool kGrad>
 __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tmem_base, int ew, int lane) {
   grid_dependency_wait();   // 2^-c_t, and the previous call's readers of the outputs
@@ -566,8 +566,8 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
           // (one token tile: tb = 0; tokens past the last one get zeros)
           const float g = col < ncol ? __ldg(p.grad + col) : 0.f;
           const bool live = g != 0.f;   // its lse and target may be anything otherwise
-          const float k2 = live ? __ldg(p.cinv + col) * 1.44269504f : 0.f;
-          const float l2 = live ? __ldg(p.lse + col) * 1.44269504f - static_cast<float>(kTcGradScale) : 0.f;
+          const float inv = live ? __ldg(p.cinv + col) : 0.f, lse = live ? __ldg(p.lse + col) : 0.f;
+          const float k2 = inv * 1.44269504f, l2 = lse * 1.44269504f - static_cast<float>(kTcGradScale);
           const int tg = live ? __ldg(p.targets + col) - p.row0 - v0 : -1;   // row within this warp's 32
           float y[32];
 #pragma unroll
@@ -576,14 +576,10 @@ __device__ void epilogue_warps(const TcParams& p, const TcSmem& sm, uint32_t tme
           for (int k = 0; k < 32; ++k)
             if (!live || k >= nrow) y[k] = 0.f;
           if (__any_sync(0xffffffffu, tg >= 0 && tg < nrow)) {
-            float own = 0.f;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (k == tg) {
-                own = y[k];
-                y[k] = 0.f;
-              }
-            if (tg >= 0 && tg < nrow) p.ptgt[col] = own * (1.f / (1 << kTcGradScale));
+              if (k == tg) y[k] = 0.f;
+            if (tg >= 0 && tg < nrow) p.ltgt[col] = fmaf(tile[lane * 33 + tg], inv, -lse);
           }
           float sum = 0.f;
 #pragma unroll

@@ -39,10 +39,10 @@ class Sure:
     """Hidden states along one row of the head each, as long as leaves the other rows the mass asked for; the target is
     that row or (every fifth token) any."""
 
-    def __init__(self, comps, T, seed):
-        V = SHAPE[0]
+    def __init__(self, comps, T, seed, shape=SHAPE):
+        V = shape[0]
         rng = np.random.default_rng(seed)
-        self.W, self.absW = oracle.dense_rows(comps, SHAPE[4], SHAPE[5])
+        self.W, self.absW = oracle.dense_rows(comps, shape[4], shape[5])
         unit = self.W / np.linalg.norm(self.W, axis=1, keepdims=True)
         along = unit @ self.W.T
         first = np.nonzero(np.diag(along) > 1.3 * np.sort(along - np.diag(np.diag(along)), axis=1)[:, -1])[0]

@@ -6,6 +6,7 @@ import torch
 
 import archead_inputs as gen
 import oracle
+from test_gpu_grad_confident import SHAPE, Sure
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,30 @@ def test_logits_of_a_shard_are_the_forwards(qoh, T, g_B, r_c, r_r):
                            torch.from_numpy(lse).cuda(), torch.from_numpy(g).cuda(), out_dtype=torch.float32)
     worst = np.abs(got.double().cpu().numpy() - want) / bound
     assert np.all(worst <= 1), worst.max()
+
+
+@pytest.mark.parametrize("g_B", [64, 32])
+@pytest.mark.parametrize("T", [1, 4, 40, 130, 300, 1100])
+def test_sure_tokens_on_shards(qoh, T, g_B):
+    """With the lse that the shards' forwards give, merged.  The rows of sure tokens (see test_gpu_grad_confident) get the
+    target's coefficient from exp(y - lse) - 1, which is as exact as y and lse agree: both are sums of the same products in
+    fp32, so off by lse's roundings (2^-22 (1 + |lse|)) and by those of K / 16 partial sums on either side, which are
+    independent: four standard deviations at most, of sqrt(K / 16) 2^-24 times sum |W| |h| each."""
+    shape = SHAPE[:5] + (g_B,)
+    comps = gen.random_components(gen.HeadShape(*shape), 31)
+    c = Sure(comps, T, 80 + T, shape)
+    h, targets, _, g = c.args()
+    shards = []
+    for v0, v1 in ((0, 1008), (1008, 2000)):
+        s = qoh.PackedHead(v1 - v0, *shape[1:], qoh.shard_components(comps, v0, v1))
+        s.set_vocab_shard(v0, shape[0])
+        shards.append(s)
+    lse, _, _ = qoh.merge_shards(torch.stack([s.shard_partials(h, targets) for s in shards]))
+    got = sum(s.grad_hidden(h, targets, lse, g, out_dtype=torch.float32) for s in shards).double().cpu().numpy()
+    products = np.einsum("ij,ij->i", np.abs(c.h), c.absW[c.targets])
+    agree = 2.0 ** -22 * (1 + np.abs(c.lse)) + 4 * np.sqrt(2 * (shape[1] + 32 + 64) / 16) * 2.0 ** -24 * products
+    rel = 5.1 * 2.0 ** -11 + shape[0] / 16 * 2.0 ** -23
+    bound = ((rel + np.expm1(2 * c.tau))[:, None] * c.terms + c.least + 2.0 ** -22 * np.abs(c.dh)
+             + (np.abs(c.g) * agree)[:, None] * c.absW[c.targets])
+    worst = (np.abs(got - c.dh) / bound).max(axis=1)
+    assert np.all(worst <= 1), (worst.max(), c.left[worst.argmax()])
